@@ -14,6 +14,8 @@ with torch and call the entry points.
 from __future__ import annotations
 
 import ctypes as C
+import functools
+import math
 import os
 
 import torch
@@ -29,13 +31,15 @@ FP4Q_OK, FP4Q_ERR_INVALID_ARG, FP4Q_ERR_UNSUPPORTED, FP4Q_ERR_ALIGNMENT, FP4Q_ER
 FP4Q_NVFP4, FP4Q_MXFP4, FP4Q_NVFP4_DUAL, FP4Q_INT4 = 0, 1, 2, 3
 FP4Q_SCALES_LINEAR, FP4Q_SCALES_SWIZZLED = 0, 1
 FP4Q_TSCALE_DYNAMIC, FP4Q_TSCALE_STATIC = 0, 1
+FP4Q_FP8_ROW, FP4Q_FP8_TILE = 0, 1
 FP4Q_WORKSPACE_BYTES = 16384
 
 EXPORTED = [
     "fp4q_quantize_nvfp4", "fp4q_quantize_nvfp4_noalloc", "fp4q_quantize_mxfp4", "fp4q_hadamard_quantize", "fp4q_arc_quantize",
     "fp4q_dequantize", "fp4q_workspace_bytes", "fp4q_scales_bytes", "fp4q_status_string",
     "fp4q_device_error", "fp4q_selftest_div", "fp4q_gemm_nvfp4", "fp4q_hadamard_quantize_signed",
-    "fp4q_dequantize_signed",
+    "fp4q_dequantize_signed", "fp4q_quantize_fp8", "fp4q_gemm_fp8", "fp4q_kv_append_fp8", "fp4q_attention_fp8",
+    "fp4q_attention_fp8_workspace_bytes",
 ]
 
 
@@ -69,12 +73,25 @@ def declare(L: C.CDLL) -> C.CDLL:
         "fp4q_gemm_nvfp4": (i32, [p, p, p, p, p, p, i64, i64, i64, p, i32, p]),
         "fp4q_hadamard_quantize_signed": (i32, [p, i64, i64, i64, i32, p, i32, p, p, p, i32, i32, p, sz, p]),
         "fp4q_dequantize_signed": (i32, [i32, p, p, p, i64, i64, i32, i32, p, p, p]),
+        "fp4q_quantize_fp8": (i32, [p, i64, i64, i64, i32, p, i64, p, i64, p, i64, p, i64, p]),
+        "fp4q_gemm_fp8": (i32, [p, i64, p, i64, p, i64, p, i64, i32, i64, i64, i64, p, i64, i32, p]),
+        "fp4q_kv_append_fp8": (i32, [p, i64, p, i64, i64, p, p, p, i64, i64, p]),
+        "fp4q_attention_fp8": (i32, [p, i64, i64, i32, p, p, p, i64, i64, i64, i32, f32, p, i64, p, p, sz, p]),
+        "fp4q_attention_fp8_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
         fn.restype = res
         fn.argtypes = args
     return L
+
+
+class Fp4qKvCache(C.Structure):
+    """fp4q_kv_cache of the header."""
+
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("num_pages", C.c_int64), ("num_kv_heads", C.c_int32), ("page_size", C.c_int32),
+                ("head_dim", C.c_int32), ("block_table", C.c_void_p), ("table_stride", C.c_int64)]
 
 
 class _Lazy:
@@ -238,6 +255,159 @@ def fp4q_selftest_div(x, d, q_fast, q_ieee, stream=None):
                                          _stream(stream)), "fp4q_selftest_div")
 
 
+# ----------------------------------------------------------------------------- 8-bit entry points
+
+def _on_device(fn):
+    """Runs the call with the first tensor's device current (the library launches on the
+    current device, and the default stream is that device's current one); the other tensors
+    have to be there too."""
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        tensors = [a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)]
+        for t in tensors:
+            if not t.is_cuda:
+                raise ValueError("fp4q entry points take CUDA tensors")
+            if t.device != tensors[0].device:
+                raise ValueError(f"{fn.__name__}: tensors on {tensors[0].device} and {t.device}")
+        if not tensors or tensors[0].device.index == torch.cuda.current_device():
+            return fn(*args, **kwargs)
+        with torch.cuda.device(tensors[0].device):
+            return fn(*args, **kwargs)
+    return call
+
+
+def _want(t, name, dtypes, *shape):
+    """A tensor argument's type and shape (None: any size) against what the call takes."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d).replace('torch.', '') for d in dtypes)}, not {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, not {tuple(t.shape)}")
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+
+
+def _row_stride(t, name):
+    """Row stride of a 2-D row-major view."""
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be a row-major view (unit column stride)")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _fp8_rows(n, block):
+    return n if block == FP4Q_FP8_ROW else -(-n // 128)
+
+
+def _fp8_side(codes, scales, rows, cols, block, what):
+    """Codes [rows, cols] and scales [ceil(cols/128), rows or tile rows]: their strides."""
+    _want(codes, f"{what} codes", _CODES, rows, cols)
+    _want(scales, f"{what} scales", _F32, -(-cols // 128), _fp8_rows(rows, block))
+    return _lead(codes, f"{what} codes", 16), _lead(scales, f"{what} scales", 4)
+
+
+def _lead(t, name, unit):
+    """The row stride; for a single row, whose stride says nothing, the next multiple of `unit`."""
+    return _row_stride(t, name) if t.shape[0] > 1 else -(-t.shape[1] // unit) * unit
+
+
+@_on_device
+def fp4q_quantize_fp8(x, block, codes=None, scales=None, codes_t=None, scales_t=None, stream=None):
+    """E4M3 codes and block-128 scales of bf16 x [M, K] and / or of its transpose."""
+    _want(x, "x", _BF16, None, None)
+    M, K = x.shape
+    ldc, lds = _fp8_side(codes, scales, M, K, block, "x") if codes is not None else (0, 0)
+    ldct, ldst = _fp8_side(codes_t, scales_t, K, M, block, "transposed") if codes_t is not None else (0, 0)
+    return _check(_lib.fp4q_quantize_fp8(_ptr(x), M, K, _lead(x, "x", 8), int(block), _ptr(codes), ldc, _ptr(scales),
+                                         lds, _ptr(codes_t), ldct, _ptr(scales_t), ldst, _stream(stream)),
+                  "fp4q_quantize_fp8")
+
+
+@_on_device
+def fp4q_gemm_fp8(a_codes, a_scales, b_codes, b_scales, b_block, d, stream=None):
+    """d [M, N] (float32 or bfloat16) = A B^T of two fp4q_quantize_fp8 outputs (A: row blocks)."""
+    _want(d, "d", (torch.float32, torch.bfloat16), None, None)
+    M, N = d.shape
+    K = a_codes.shape[-1]
+    lda, ldas = _fp8_side(a_codes, a_scales, M, K, FP4Q_FP8_ROW, "A")
+    ldb, ldbs = _fp8_side(b_codes, b_scales, N, K, b_block, "B")
+    return _check(_lib.fp4q_gemm_fp8(_ptr(a_codes), lda, _ptr(a_scales), ldas, _ptr(b_codes), ldb, _ptr(b_scales), ldbs,
+                                     int(b_block), M, N, K, _ptr(d), _row_stride(d, "d"),
+                                     int(d.dtype == torch.bfloat16), _stream(stream)), "fp4q_gemm_fp8")
+
+
+def _token_stride(t, name):
+    """Stride between tokens of [tokens, heads, dim] whose heads and dims are contiguous."""
+    T, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: heads and dims of a token must be contiguous")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table):
+    _want(k_cache, "k_cache", _CODES, None, None, None, None)
+    pages, heads, page, dim = k_cache.shape
+    _want(v_cache, "v_cache", _CODES, pages, heads, page, dim)
+    _want(k_scale, "k_scale", _F32, pages, heads)
+    _want(v_scale, "v_scale", _F32, pages, heads)
+    _want(block_table, "block_table", _I32, None, None)
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"),
+                 (block_table, "block_table")):
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    return Fp4qKvCache(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), pages, heads, page, dim,
+                       _ptr(block_table), block_table.shape[1])
+
+
+def _ragged(cu, lens, block_table, name):
+    B = block_table.shape[0]
+    _want(cu, name, _I32, B + 1)
+    _want(lens, "lens", _I32, B)
+    if not (cu.is_contiguous() and lens.is_contiguous()):
+        raise ValueError(f"{name} and lens must be contiguous")
+    return B
+
+
+@_on_device
+def fp4q_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, lens, max_new, stream=None):
+    """Writes the new tokens k, v [tokens, Hkv, D] (bf16) at the end of their sequences."""
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+    _want(k, "k", _BF16, None, cache.num_kv_heads, cache.head_dim)
+    _want(v, "v", _BF16, *k.shape)
+    B = _ragged(cu_new, lens, block_table, "cu_new")
+    return _check(_lib.fp4q_kv_append_fp8(_ptr(k), _token_stride(k, "k"), _ptr(v), _token_stride(v, "v"), k.shape[0],
+                                          C.addressof(cache), _ptr(cu_new), _ptr(lens), B, int(max_new),
+                                          _stream(stream)), "fp4q_kv_append_fp8")
+
+
+def fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, num_q_heads, num_kv_heads, head_dim):
+    n = int(_lib.fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, num_q_heads, num_kv_heads, head_dim))
+    if n == C.c_size_t(-1).value:
+        raise Fp4qError(FP4Q_ERR_INVALID_ARG, "fp4q_attention_fp8_workspace_bytes")
+    return n
+
+
+@_on_device
+def fp4q_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, max_q, max_len, o, lse=None,
+                       causal=True, softmax_scale=None, workspace=None, stream=None):
+    """o [tokens, Hq, D] (bf16) = attention of q [tokens, Hq, D] (bf16) over the cache."""
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+    _want(q, "q", _BF16, None, None, cache.head_dim)
+    _want(o, "o", _BF16, *q.shape)
+    T, Hq, D = q.shape
+    B = _ragged(cu_q, lens, block_table, "cu_q")
+    if lse is not None:
+        _want(lse, "lse", _F32, T, Hq)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+    scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return _check(_lib.fp4q_attention_fp8(_ptr(q), _token_stride(q, "q"), T, Hq, C.addressof(cache), _ptr(cu_q),
+                                          _ptr(lens), B, int(max_q), int(max_len), int(bool(causal)), scale, _ptr(o),
+                                          _token_stride(o, "o"), _ptr(lse), _ptr(workspace), ws_bytes,
+                                          _stream(stream)), "fp4q_attention_fp8")
+
+
 # ----------------------------------------------------------------------------- allocating helpers
 
 def _block(fmt: int) -> int:
@@ -336,3 +506,61 @@ def gemm_nvfp4(a_codes, a_scales, a_scale, b_codes, b_scales, b_scale, K, out_dt
     d = torch.empty((a_codes.shape[0], b_codes.shape[0]), dtype=out_dtype, device=a_codes.device)
     fp4q_gemm_nvfp4(a_codes, a_scales, a_scale, b_codes, b_scales, b_scale, K, d)
     return d
+
+
+def alloc_fp8(rows, cols, block=FP4Q_FP8_ROW, device="cuda"):
+    """codes [rows, cols] u8 and scales [ceil(cols/128), rows or ceil(rows/128)] f32, as views of
+    buffers whose rows are 16-byte aligned."""
+    n = _fp8_rows(rows, block)
+    codes = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=device)[:, :cols]
+    scales = torch.empty((-(-cols // 128), -(-n // 4) * 4), dtype=torch.float32, device=device)[:, :n]
+    return codes, scales
+
+
+def quantize_fp8(x, block=FP4Q_FP8_ROW, transpose=False):
+    """(codes, scales) of bf16 x [M, K]; with transpose=True also those of its transpose:
+    (codes, scales, codes_t, scales_t), all from one read of x."""
+    M, K = x.shape
+    out = alloc_fp8(M, K, block, x.device) + (alloc_fp8(K, M, block, x.device) if transpose else ())
+    fp4q_quantize_fp8(x, block, *out)
+    return out
+
+
+def gemm_fp8(a_codes, a_scales, b_codes, b_scales, b_block=FP4Q_FP8_TILE, out_dtype=torch.bfloat16):
+    """Allocates D [M, N] and calls fp4q_gemm_fp8."""
+    d = torch.empty((a_codes.shape[0], b_codes.shape[0]), dtype=out_dtype, device=a_codes.device)
+    fp4q_gemm_fp8(a_codes, a_scales, b_codes, b_scales, b_block, d)
+    return d
+
+
+def alloc_kv_cache(num_pages, num_kv_heads, page_size, head_dim, device="cuda"):
+    """k_cache, v_cache (u8 [num_pages, Hkv, page_size, D]) and k_scale, v_scale (f32 [num_pages, Hkv])."""
+    codes = [torch.zeros((num_pages, num_kv_heads, page_size, head_dim), dtype=torch.uint8, device=device)
+             for _ in range(2)]
+    scales = [torch.zeros((num_pages, num_kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+    return (*codes, *scales)
+
+
+def kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, lens, max_new):
+    """fp4q_kv_append_fp8; returns the cache tensors, updated in place."""
+    fp4q_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, lens, max_new)
+    return k_cache, v_cache, k_scale, v_scale
+
+
+def attention_fp8_workspace(q, k_cache, batch, max_q, max_len):
+    """Scratch for attention_fp8 calls of these sizes (None: none is needed)."""
+    with torch.cuda.device(q.device):
+        n = fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, q.shape[1], k_cache.shape[1], k_cache.shape[3])
+    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, max_q, max_len, causal=True,
+                  softmax_scale=None, ws=None):
+    """(o [tokens, Hq, D] bf16, lse [tokens, Hq] f32); tokens that belong to no sequence are left unset."""
+    o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = attention_fp8_workspace(q, k_cache, block_table.shape[0], max_q, max_len)
+    fp4q_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, max_q, max_len, o, lse, causal,
+                       softmax_scale, ws)
+    return o, lse

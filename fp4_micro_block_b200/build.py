@@ -33,7 +33,6 @@ FLAGS = [
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC,-fvisibility=hidden",
     "-Xptxas", "-v",
-    "-shared",
 ]
 
 
@@ -63,13 +62,27 @@ def build(force: bool = False, verbose: bool = False, test_hooks: bool = False,
         return lib
     tmp = lib + f".tmp{os.getpid()}"
     extra = (["-DFP4Q_TEST_HOOKS"] if test_hooks else []) + [f"-D{d}" for d in defines]
-    cmd = [nvcc(), *FLAGS, *extra, "-I", os.path.join(ROOT, "include"), os.path.join(CSRC, "fp4q.cu"),
-           "-o", tmp]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    log = res.stdout + res.stderr
+    units = [s for s in sources() if s.endswith(".cu")]
+    objs = [f"{tmp}.{os.path.basename(u)}.o" for u in units]
+    cmds = [[nvcc(), *FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-c", u, "-o", o]
+            for u, o in zip(units, objs)]
+    link = [nvcc(), *FLAGS[:2], "-shared", *objs, "-o", tmp]
+    try:
+        procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in cmds]
+        outs = [p.communicate()[0] for p in procs]  # the translation units compile side by side
+        failed = any(p.returncode != 0 for p in procs)
+        if not failed:
+            res = subprocess.run(link, capture_output=True, text=True)
+            outs.append(res.stdout + res.stderr)
+            failed = res.returncode != 0
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
+    log = "".join(" ".join(c) + "\n" + t for c, t in zip(cmds + [link], outs))
     with open(os.path.join(PKG, "build_test.log" if test_hooks else "build.log"), "w") as f:
-        f.write(" ".join(cmd) + "\n" + log)
-    if res.returncode != 0:
+        f.write(log)
+    if failed:
         raise RuntimeError("nvcc failed:\n" + log[-8000:])
     if verbose:
         print(log)

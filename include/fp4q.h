@@ -299,13 +299,149 @@ fp4q_status fp4q_dequantize_signed(fp4q_format format, const uint8_t* codes, con
                                    fp4q_scale_layout layout, int inv_had_size, const uint32_t* signs,
                                    void* y, fp4q_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit companions: E4M3 codes under one FP32 scale per block of 128 (for the
+ * tensors that do not stand 4 bits), their GEMM, and a paged K/V cache in the
+ * same codes with the attention that reads it.  (The pages name NVFP4's E4M3
+ * scales and an FP8 baseline but no FP8 path; these have no page counterpart.)
+ *
+ * Numeric rules:
+ *  - E4M3 rounding: nearest value, ties to the even code, saturating at +-448,
+ *    sign kept; a NaN gives the NaN code 0x7f.
+ *  - Blocks: s = amax/448 (IEEE binary32 division), code = E4M3(x/s) with x/s
+ *    correctly rounded; s == 0 gives zero codes.  The maximum skips NaN; a block
+ *    that holds an infinity has s = inf and dequantizes to NaN.
+ *  - Cache pages: the scale is the smallest power of two s >= amax/448 (at
+ *    least 2^-126; 0 for a page of zeros), so a page whose scale grows moves
+ *    its codes by an exact power of two (rounded again only where they become
+ *    E4M3 subnormals).
+ * --------------------------------------------------------------------------- */
+typedef enum fp4q_fp8_block {
+    FP4Q_FP8_ROW = 0, /* blocks of 1 row x 128 columns: scales [ceil(K/128), rows]             */
+    FP4Q_FP8_TILE = 1 /* blocks of 128 x 128: scales [ceil(K/128), ceil(rows/128)]              */
+} fp4q_fp8_block;
+
+/* fp4q_quantize_fp8 -- E4M3 codes and block-128 scales of a bf16 matrix and / or
+ * of its transpose (the operand of a weight or input gradient), in one read of x.
+ *   x        bf16 [M, ldx], K columns used; any M >= 0, K >= 1.  (read)
+ *   block    FP4Q_FP8_ROW or FP4Q_FP8_TILE.
+ *   codes    uint8 [M, ldc], K columns written; NULL: not wanted.
+ *   scales   float [ceil(K/128), lds]: the scale of (block kb, row m) at
+ *            kb * lds + m (TILE: kb * lds + m/128).  Columns past the last row
+ *            (tile row) are not written.
+ *   codes_t  uint8 [K, ldct], M columns written: the codes of the transpose,
+ *            whose blocks run along M (ROW: 128 rows of one column; TILE: the
+ *            same tiles).  NULL: not wanted.
+ *   scales_t float [ceil(M/128), ldst]: (block mb, column k) at mb * ldst + k
+ *            (TILE: mb * ldst + k/128).
+ * Requires at least one of the two outputs, ldx % 8 == 0, ldc and ldct
+ * multiples of 16 and >= K and M, lds and ldst multiples of 4 and >= the rows
+ * (tile rows) they index; x, codes, scales 16-byte aligned. */
+fp4q_status fp4q_quantize_fp8(const void* x, int64_t M, int64_t K, int64_t ldx, fp4q_fp8_block block,
+                              uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
+                              uint8_t* codes_t, int64_t ldct, float* scales_t, int64_t ldst,
+                              fp4q_stream_t stream);
+
+/* fp4q_gemm_fp8 -- block-scaled FP8 GEMM on the tensor cores,
+ *   D[m, n] = sum over blocks kb of SA[kb, m] * SB[kb, n] *
+ *             sum over k in kb of E4M3(A[m, k]) * E4M3(B[n, k])
+ * with FP32 sums.
+ *   a_codes   uint8 [M, lda], a_scales float [ceil(K/128), ldas] (FP4Q_FP8_ROW).
+ *   b_codes   uint8 [N, ldb], b_scales float [ceil(K/128), ldbs], of FP4Q_FP8_ROW
+ *             or FP4Q_FP8_TILE blocks (b_block).
+ *   d         [M, ldd] row-major, N columns written: FP32 (d_bf16 = 0) or bf16
+ *             rounded to nearest even (d_bf16 = 1).
+ * Linear layer y = x W^T: A = x (ROW), B = W (TILE).  Input gradient: A = dy
+ * (ROW), B = W^T (codes_t / scales_t of W).  Weight gradient: A = dy^T, B = x^T
+ * (codes_t / scales_t, ROW).
+ * Any M >= 0, N >= 1, K >= 1; bytes past column K of a row are not used.
+ * Requires lda, ldb >= K and multiples of 16, ldas >= M and ldbs >= N (TILE:
+ * ceil(N/128)) multiples of 4, ldd >= N; 16-byte aligned codes, scales and d. */
+fp4q_status fp4q_gemm_fp8(const uint8_t* a_codes, int64_t lda, const float* a_scales, int64_t ldas,
+                          const uint8_t* b_codes, int64_t ldb, const float* b_scales, int64_t ldbs,
+                          fp4q_fp8_block b_block, int64_t M, int64_t N, int64_t K, void* d, int64_t ldd,
+                          int d_bf16, fp4q_stream_t stream);
+
+/* A paged K/V cache in 8 bits.  Page p of K holds page_size tokens of every
+ * K/V head: codes uint8 [num_pages, num_kv_heads, page_size, head_dim], scales
+ * float [num_pages, num_kv_heads] (value = E4M3(code) * scale); V likewise.
+ * Position t of sequence b lives in page block_table[b * table_stride +
+ * t / page_size], row t % page_size.  page_size is 16, 32, 64 or 128; head_dim
+ * 64, 128 or 256. */
+typedef struct fp4q_kv_cache {
+    uint8_t* k;       /* 16-byte aligned                          */
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t num_pages;
+    int32_t num_kv_heads;
+    int32_t page_size;
+    int32_t head_dim;
+    const int32_t* block_table; /* [batch, table_stride]          */
+    int64_t table_stride;       /* pages a sequence may have      */
+} fp4q_kv_cache;
+
+/* fp4q_kv_append_fp8 -- writes new tokens' K and V into the cache.
+ *   k, v     bf16 [tokens, num_kv_heads, head_dim], token strides ldk, ldv in
+ *            elements (multiples of 8).
+ *   cu_new   int32 [batch + 1]: sequence b's new tokens are rows
+ *            cu_new[b] .. cu_new[b + 1] - 1 of k and v.  Rows outside are not read.
+ *   lens     int32 [batch]: sequence b's length after the call; its new tokens
+ *            take the last positions before it.
+ *   max_new  no sequence has more new tokens than this.
+ * A page's scale covers the tokens it holds: when new tokens begin the page it
+ * starts afresh (what the page held before does not count), otherwise it grows
+ * if the new tokens need it and the codes before them move to the new scale.
+ * Rows of a page past the sequence's end are left as they are.
+ * The pages written belong to one sequence each (a caller that shares pages
+ * between sequences copies the last, partly filled one first).
+ * Entries out of range on the device (a page id outside [0, num_pages), a
+ * position outside the table, cu_new outside [0, tokens] or above max_new) are
+ * skipped and reported through fp4q_device_error(), code 2. */
+fp4q_status fp4q_kv_append_fp8(const void* k, int64_t ldk, const void* v, int64_t ldv, int64_t tokens,
+                               const fp4q_kv_cache* cache, const int32_t* cu_new, const int32_t* lens,
+                               int64_t batch, int64_t max_new, fp4q_stream_t stream);
+
+/* fp4q_attention_fp8 -- attention of bf16 queries over the cache,
+ *   o[i, h] = sum_j softmax_j(softmax_scale * q[i, h] . k[j, h / G]) v[j, h / G],
+ * G = num_q_heads / num_kv_heads.
+ *   q        bf16 [tokens, num_q_heads, head_dim], token stride ldq (multiple of 8).
+ *   cu_q     int32 [batch + 1]: sequence b's queries are rows cu_q[b] .. cu_q[b + 1] - 1.
+ *   lens     int32 [batch]: cached tokens of sequence b (the queries' own
+ *            included, written before by fp4q_kv_append_fp8).
+ *   max_q, max_len  no sequence has more queries / cached tokens than these.
+ *   causal   1: query i of n sees keys j <= lens[b] - n + i; 0: all lens[b] keys.
+ *   o        bf16 [tokens, num_q_heads, head_dim], token stride ldo (multiple of 8).
+ *   lse      float [tokens, num_q_heads], the natural logarithm of the sum of
+ *            exponentials; NULL: not wanted.
+ *   workspace  >= fp4q_attention_fp8_workspace_bytes() device bytes, 16-byte
+ *            aligned; calls that may overlap need one each.
+ * A query that sees no key gets o = 0 and lse = -inf.  Rows of o and lse outside
+ * cu_q's ranges are left as they are.  Codes of masked keys, NaN codes among
+ * them, do not reach a result.  Sums and softmax statistics are FP32; the
+ * probabilities enter the product with V in FP16 under a common exponent.
+ * Entries out of range on the device are clamped (a page id outside
+ * [0, num_pages) reads page 0) and reported through fp4q_device_error(), code 2. */
+fp4q_status fp4q_attention_fp8(const void* q, int64_t ldq, int64_t tokens, int32_t num_q_heads,
+                               const fp4q_kv_cache* cache, const int32_t* cu_q, const int32_t* lens,
+                               int64_t batch, int64_t max_q, int64_t max_len, int causal,
+                               float softmax_scale, void* o, int64_t ldo, float* lse, void* workspace,
+                               size_t workspace_bytes, fp4q_stream_t stream);
+
+/* Device scratch fp4q_attention_fp8 needs for these sizes (0: none; the
+ * workspace may then be NULL).  Depends on the current device's SM count.
+ * Returns (size_t)-1 on bad arguments. */
+size_t fp4q_attention_fp8_workspace_bytes(int64_t batch, int64_t max_q, int64_t max_len,
+                                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fp4q_status_string(fp4q_status status);
 
 /* Reads and clears the device error word of the CURRENT device: 0 if no kernel
  * recorded an error since the last read, else a bit mask (1 = a bounded wait
  * on a tile's arrival barrier ran out; 2 = an index argument of
- * fp4q_arc_quantize was outside [0, K) and was clamped).  Synchronizes the
+ * fp4q_arc_quantize was outside [0, K) and was clamped, or an entry of a block
+ * table, length or offset array of the 8-bit cache calls was out of range).  Synchronizes the
  * device.  Returns -1 if the read itself failed. */
 int fp4q_device_error(void);
 

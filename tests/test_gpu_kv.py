@@ -1,0 +1,451 @@
+"""The paged 8-bit K/V cache, its writer and the attention over it, against the oracle, on a GPU.
+
+Append: bit-exact codes and scales.
+
+Attention tolerance, per query, head and column (p = the exact probabilities):
+ - the output's rounding, half a bf16 step: 2^-8 |o|;
+ - the logits: a D-long fp32 sum of products that are exact (bf16 x E4M3) but
+   for chopping, at most (D + 8) 2^-23 of R = max_j scale * sum |q| |k_j|, which
+   moves a probability by twice that, relative (numerator and denominator);
+ - each probability's rounding to fp16 (2^-11 relative) and its exponential
+   (2 units in the last place, and those of its argument: 2^-22 + R 2^-22);
+ - the fp32 sums over the keys: len 2^-23;
+all of sum_j p_j |v_j|.  Probabilities below fp16's normals are off by at most
+2^-25 of the largest weight: len 2^-25 max |v|.
+lse: the logits' part, the exponentials' and the sum's, and its own rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8
+from parity import bf16_torch_to_bits, to_np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fq():
+    from fp4_micro_block_b200 import build
+    build.build()
+    import fp4_micro_block_b200 as m
+    assert m.fp4q_device_error() == 0
+    yield m
+    assert m.fp4q_device_error() == 0
+
+
+def host(t):
+    return fp8.bf16_values(bf16_torch_to_bits(t))
+
+
+def bf16(rng, *shape, gain=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * gain).astype(np.float32)).to(torch.bfloat16).cuda()
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def cum(ns):
+    return [0] + list(np.cumsum(ns))
+
+
+def table_for(rng, lens, page, pool, width=None):
+    """Distinct random pages for each sequence; unused entries hold an id that must not be read."""
+    need = [-(-n // page) for n in lens]
+    ids = rng.permutation(pool)[:sum(need)]
+    t = np.full((len(lens), width or max(need + [1])), 2 ** 30, np.int32)
+    at = 0
+    for i, n in enumerate(need):
+        t[i, :n] = ids[at:at + n]
+        at += n
+    return t
+
+
+def random_cache(rng, pool, heads, page, D, spread=2.0):
+    """Codes of every value but NaN, page scales over a few octaves, powers of two and not."""
+    out = []
+    for _ in range(2):
+        c = rng.integers(0, 256, (pool, heads, page, D)).astype(np.uint8)
+        c[(c & 0x7F) > 0x70] &= 0x8F  # mostly moderate magnitudes, none of them NaN
+        out.append(c)
+    for _ in range(2):
+        out.append((np.exp2(rng.uniform(-spread, spread, (pool, heads))) / 64).astype(np.float32))
+    return out
+
+
+def up(arrays):
+    return [torch.from_numpy(np.array(a)).cuda() for a in arrays]
+
+
+# ------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("D,heads", [(64, 1), (128, 2), (256, 3)])
+def test_append(fq, page, D, heads):
+    """Sequences that begin, end and go on inside pages, at page borders, with nothing new, of one token and many."""
+    rng = np.random.default_rng(page + D)
+    new = [1, 0, page, page + 1, 3 * page - 5, 7, 2, 1]
+    old = [0, 40, page, page - 1, 5, 2 * page - 3, page, page - 1]
+    lens = [n + o for n, o in zip(new, old)]
+    pool = sum(-(-n // page) for n in lens) + 2
+    cache = random_cache(rng, pool, heads, page, D)
+    for s in cache[2:]:
+        s[:] = np.exp2(rng.integers(-9, -5, s.shape))
+        s[::5] = 0.0  # pages of zeros so far
+    cache[0][cache[2] == 0] = 0
+    cache[1][cache[3] == 0] = 0
+    table = table_for(rng, lens, page, pool)
+    k, v = bf16(rng, sum(new) + 3, heads, D), bf16(rng, sum(new) + 3, heads, D, gain=0.01)
+    dev = up(cache)
+    fq.kv_append_fp8(k, v, *dev, i32(table.tolist()), i32(cum(new)), i32(lens), max(new))
+    want = fp8.kv_append(host(k), host(v), cache, table, cum(new), lens)
+    for got, w, name in zip(dev, want, ("k", "v", "k_scale", "v_scale")):
+        assert np.array_equal(to_np(got), w), name
+
+
+def test_append_token_by_token(fq):
+    """A growing sequence: every step equals the oracle's, and rows past the end keep what they held."""
+    rng = np.random.default_rng(3)
+    page, D, heads = 16, 64, 2
+    cache = random_cache(rng, 4, heads, page, D)
+    dev = up(cache)
+    table = np.array([[2, 0, 3]], np.int32)
+    for t in range(36):
+        k, v = bf16(rng, 1, heads, D, gain=1.1 ** t), bf16(rng, 1, heads, D, gain=1.0 / (1 + t))
+        fq.kv_append_fp8(k, v, *dev, i32(table.tolist()), i32([0, 1]), i32([t + 1]), 1)
+        cache = fp8.kv_append(host(k), host(v), cache, table, [0, 1], [t + 1])
+    for got, w in zip(dev, cache):
+        assert np.array_equal(to_np(got), w)
+
+
+def test_append_strided_and_extreme_values(fq):
+    """K and V as slices of one projection; zeros, subnormals, the largest values, NaN and infinities."""
+    rng = np.random.default_rng(5)
+    page, D, heads, n = 32, 128, 2, 70
+    qkv = bf16(rng, n, 4 * heads, D)
+    qkv[:32, :, :] = 0
+    qkv[40, heads, 3] = float("nan")
+    qkv[64:, heads:, :] *= 1e-38
+    qkv[33, 2 * heads, 5] = 3.0e38
+    k, v = qkv[:, heads:2 * heads], qkv[:, 2 * heads:3 * heads]
+    cache = [np.zeros((5, heads, page, D), np.uint8) for _ in range(2)] + [np.ones((5, heads), np.float32) for _ in range(2)]
+    table = np.array([[4, 1, 2]], np.int32)
+    dev = up(cache)
+    fq.kv_append_fp8(k, v, *dev, i32(table.tolist()), i32([0, n]), i32([n]), n)
+    want = fp8.kv_append(host(k.contiguous()), host(v.contiguous()), cache, table, [0, n], [n])
+    for got, w in zip(dev, want):
+        assert np.array_equal(to_np(got), w)
+    inf = qkv[:1, :heads].clone()
+    inf[0, 0, 0] = float("inf")
+    dev = up(cache)
+    fq.kv_append_fp8(inf, inf, *dev, i32(table.tolist()), i32([0, 1]), i32([1]), 1)
+    assert float(dev[2][4, 0]) == 2.0 ** 120 and int(dev[0][4, 0, 0, 0]) == 0x7E
+
+
+def test_append_reports_entries_out_of_range(fq):
+    """Bad page ids, positions past the table and offsets past the tokens write nothing and are reported."""
+    rng = np.random.default_rng(6)
+    page, D, heads = 16, 64, 1
+    cache = random_cache(rng, 3, heads, page, D)
+    k = bf16(rng, 4, heads, D)
+    assert fq.fp4q_device_error() == 0
+    for table, cu, lens, most in (([[3]], [0, 1], [1], 1), ([[-1]], [0, 1], [1], 1), ([[0]], [0, 1], [17], 1),
+                                  ([[0]], [0, 5], [5], 8), ([[0]], [0, 3], [3], 2), ([[0]], [0, 2], [1], 2),
+                                  ([[0]], [2, 1], [1], 2), ([[0]], [-1, 1], [2], 2)):
+        dev = up(cache)
+        fq.kv_append_fp8(k, k, *dev, i32(table), i32(cu), i32(lens), most)
+        assert fq.fp4q_device_error() == 2, (table, cu, lens)
+        for got, w in zip(dev, cache):
+            assert np.array_equal(to_np(got), w)
+
+
+# ------------------------------------------------------------------ attention
+
+def run(fq, rng, new, lens, page, D, heads, G, causal=True, cache=None, pool=None, q=None, **kw):
+    pool = pool or sum(-(-n // page) for n in lens) + 1
+    cache = random_cache(rng, pool, heads, page, D) if cache is None else cache
+    table = table_for(rng, lens, page, pool)
+    cu = cum(new)
+    q = bf16(rng, cu[-1], heads * G, D) if q is None else q
+    # codes past the sequences' ends are NaN: they must not be seen
+    for b, n in enumerate(lens):
+        if n % page:
+            cache[0][table[b, n // page], :, n % page:] = 0x7F
+            cache[1][table[b, n // page], :, n % page:] = 0xFF
+    dev = up(cache)
+    o, lse = fq.attention_fp8(q, *dev, i32(table.tolist()), i32(cu), i32(lens), max(new), max(lens), causal, **kw)
+    compare(o, lse, q, cache, table, cu, lens, causal, kw.get("softmax_scale") or D ** -0.5)
+    return o, lse, q, dev, table, cu
+
+
+def compare(o, lse, q, cache, table, cu, lens, causal, scale):
+    D = q.shape[2]
+    want, want_lse, pv, reach, vmax = fp8.attention(host(q), cache, table, cu, lens, causal, scale)
+    most = max(list(lens) + [1])
+    logits = (D + 8) * 2.0 ** -23 * reach
+    rel = 2 * logits + 2.0 ** -11 + 2.0 ** -22 + reach * 2.0 ** -22 + most * 2.0 ** -23
+    tol = 2.0 ** -8 * np.abs(want) + (1 + 2.0 ** -8) * (rel[..., None] * pv + most * 2.0 ** -25 * vmax[..., None]) + 1e-38
+    off = np.abs(to_np(o.double()) - want)
+    assert np.isfinite(to_np(o.float())).all() and (off <= tol).all(), \
+        f"{int((off > tol).sum())} of {off.size} off, worst {np.nanmax(off / tol)} of the tolerance"
+    got, none = to_np(lse.double()), np.isneginf(want_lse)
+    assert np.array_equal(np.isneginf(got), none)
+    ltol = logits + 2.0 ** -21 + reach * 2.0 ** -22 + most * 2.0 ** -23 + 2.0 ** -22 * np.abs(want_lse)
+    assert (np.abs(got - want_lse)[~none] <= ltol[~none]).all()
+    assert (to_np(o.float())[none] == 0).all()
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_single_tokens(fq, D, page):
+    rng = np.random.default_rng(D + page)
+    lens = [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 300, 511, 900]
+    run(fq, rng, [1] * len(lens), lens, page, D, 2, 4)
+
+
+@pytest.mark.parametrize("heads,G", [(1, 1), (1, 8), (3, 5), (2, 16), (1, 20), (8, 1)])
+def test_head_layouts(fq, heads, G):
+    rng = np.random.default_rng(heads * 100 + G)
+    run(fq, rng, [1, 1, 3], [70, 333, 12], 32, 128, heads, G)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,page,G", [(64, 16, 1), (128, 64, 4), (128, 128, 3), (256, 32, 2)])
+def test_several_queries(fq, D, page, G, causal):
+    """From the few tokens of a speculative step to chunks of a prompt, alone and over a cached prefix; sequences
+    without queries, without keys, and with more queries than keys (rows that see nothing)."""
+    rng = np.random.default_rng(D + page + G)
+    run(fq, rng, [2, 5, 0, 17, 40, 130, 3, 9, 1], [2, 64, 50, 17, 200, 131, 0, 4, 77], page, D, 2, G, causal)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_lengths_around_tiles(fq, D):
+    rng = np.random.default_rng(D)
+    run(fq, rng, [127, 128, 129, 64, 63, 65, 256, 255], [127, 128, 129, 200, 300, 65, 256, 400], 64, D, 1, 2)
+
+
+@pytest.mark.parametrize("B", [1, 3])
+def test_long_sequences(fq, B):
+    rng = np.random.default_rng(11)
+    run(fq, rng, [1] * B, [20000, 9000, 13][:B], 64, 128, 1, 4)
+
+
+def test_softmax_scale_and_peaked_rows(fq):
+    """A scale far from 1/sqrt(D): one key holds nearly all the weight, and a negative one."""
+    rng = np.random.default_rng(12)
+    for scale in (1.0, -0.3, 1e-6):
+        run(fq, rng, [1, 4], [500, 100], 32, 64, 2, 2, softmax_scale=scale)
+
+
+def test_page_scales_far_apart(fq):
+    """Pages whose V scales differ by many octaves, zero scales among them, with the weight on the small ones."""
+    rng = np.random.default_rng(13)
+    page, D, heads, pool = 32, 64, 1, 12
+    cache = random_cache(rng, pool, heads, page, D)
+    cache[3][:, 0] = np.exp2(-6.0 * np.arange(pool)).astype(np.float32)
+    cache[2][:, 0] = np.linspace(0.02, 0.2, pool).astype(np.float32)
+    cache[3][5] = 0.0
+    cache[2][7] = 0.0
+    run(fq, rng, [1, 3], [300, 40], page, D, heads, 2, cache=cache, pool=pool)
+
+
+def test_values_of_one_page_only_small(fq):
+    """Every visible V scale far below one: the result is as exact as with ordinary ones."""
+    rng = np.random.default_rng(14)
+    cache = random_cache(rng, 8, 1, 32, 128)
+    cache[3][:] = 2.0 ** -90
+    run(fq, rng, [1, 20], [100, 60], 32, 128, 1, 2, cache=cache, pool=8)
+
+
+@pytest.mark.parametrize("new", [1, 4, 40, 150])
+def test_masked_nan_does_not_leak(fq, new):
+    """A NaN in the last token's K and V reaches only the last query, which sees it."""
+    rng = np.random.default_rng(15 + new)
+    page, D, heads, G, L = 32, 128, 1, 2, 200
+    pool = 8
+    cache = random_cache(rng, pool, heads, page, D)
+    table = table_for(rng, [L], page, pool)
+    q = bf16(rng, new, heads * G, D)
+    clean = fq.attention_fp8(q, *up(cache), i32(table.tolist()), i32([0, new]), i32([L]), new, L)
+    for side in (0, 1):
+        broken = [c.copy() for c in cache]
+        broken[side][table[0, (L - 1) // page], 0, (L - 1) % page, 3] = 0x7F
+        o, _ = fq.attention_fp8(q, *up(broken), i32(table.tolist()), i32([0, new]), i32([L]), new, L)
+        assert torch.equal(o[:-1], clean[0][:-1])
+        last = to_np(o[-1].float())
+        if side == 0:
+            assert np.isnan(last).all()
+        else:
+            assert np.isnan(last[:, 3]).all() and np.isfinite(np.delete(last, 3, 1)).all()
+
+
+def test_rows_outside_the_sequences_are_left(fq):
+    rng = np.random.default_rng(16)
+    page, D, heads, G = 16, 64, 2, 2
+    cache = random_cache(rng, 6, heads, page, D)
+    table = table_for(rng, [20, 30], page, 6)
+    q = bf16(rng, 12, heads * G, D)
+    o = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    cu = [2, 5, 9]
+    dev = up(cache)
+    ws = fq.attention_fp8_workspace(q, dev[0], 2, 4, 30)
+    fq.fp4q_attention_fp8(q, *dev, i32(table.tolist()), i32(cu), i32([20, 30]), 4, 30, o, lse, workspace=ws)
+    assert (o[:2] == 7).all() and (o[9:] == 7).all() and (lse[:2] == 7).all() and (lse[9:] == 7).all()
+    part, part_lse = fq.attention_fp8(q[2:9].contiguous(), *dev, i32(table.tolist()), i32([0, 3, 7]), i32([20, 30]), 4, 30)
+    assert torch.equal(o[2:9], part) and torch.equal(lse[2:9], part_lse)
+
+
+def test_views_and_no_lse(fq):
+    """Queries as a slice of a fused projection, outputs into a slice of a wider buffer."""
+    rng = np.random.default_rng(17)
+    page, D, heads, G = 64, 128, 2, 4
+    for new, lens in (([1, 1], [100, 900]), ([30, 1], [100, 40])):
+        o, lse, q, dev, table, cu = run(fq, rng, new, lens, page, D, heads, G)
+        wide = torch.zeros((cu[-1], heads * G + 2 * heads, D), dtype=torch.bfloat16, device="cuda")
+        wide[:, :heads * G] = q
+        out = torch.full((cu[-1], heads * G + 3, D), 5.0, dtype=torch.bfloat16, device="cuda")
+        ws = fq.attention_fp8_workspace(q, dev[0], 2, max(new), max(lens))
+        fq.fp4q_attention_fp8(wide[:, :heads * G], *dev, i32(table.tolist()), i32(cu), i32(lens), max(new), max(lens),
+                              out[:, :heads * G], workspace=ws)
+        assert torch.equal(out[:, :heads * G], o) and (out[:, heads * G:] == 5).all()
+
+
+def test_bounds_given_larger_than_the_lengths(fq):
+    """max_q and max_len may exceed what the sequences have (a graph captured for the largest batch)."""
+    rng = np.random.default_rng(18)
+    lens, new = [5, 700, 64], [1, 2, 1]
+    _, _, q, dev, table, cu = run(fq, rng, new, lens, 32, 64, 2, 2)
+    for most_q, most in ((7, 64 * 32), (40, 5000)):
+        wide = np.zeros((3, 160), np.int32)
+        wide[:, :table.shape[1]] = table
+        o, lse = fq.attention_fp8(q, *dev, i32(wide.tolist()), i32(cu), i32(lens), most_q, most)
+        compare(o, lse, q, [to_np(t) for t in dev], table, cu, lens, True, 64 ** -0.5)
+
+
+def test_entries_out_of_range_are_reported(fq):
+    rng = np.random.default_rng(19)
+    page, D, heads = 16, 64, 1
+    cache = random_cache(rng, 3, heads, page, D)
+    dev = up(cache)
+    assert fq.fp4q_device_error() == 0
+    for n in (1, 20):
+        q = bf16(rng, n, 2, D)
+        for table, cu, lens, most_q, most in (([[1, 3]], [0, n], [20], n, 32), ([[1, -5]], [0, n], [20], n, 32),
+                                              ([[1, 2]], [0, n], [40], n, 64), ([[1, 2]], [0, n], [32], n, 20),
+                                              ([[1, 2]], [0, n + 1], [20], n + 1, 32), ([[1, 2]], [0, n], [-1], n, 32),
+                                              ([[1, 2]], [-1, n], [20], n + 1, 32)):
+            fq.attention_fp8(q, *dev, i32(table), i32(cu), i32(lens), most_q, most)
+            assert fq.fp4q_device_error() == 2, (table, cu, lens)
+
+
+def test_workspace_refusals(fq):
+    rng = np.random.default_rng(20)
+    cache = up(random_cache(rng, 80, 1, 64, 128))
+    q = bf16(rng, 1, 4, 128)
+    n = fq.fp4q_attention_fp8_workspace_bytes(1, 1, 5000, 4, 1, 128)
+    args = (q, *cache, i32([list(range(79))]), i32([0, 1]), i32([5000]), 1, 5000, torch.empty_like(q))
+    if n:
+        with pytest.raises(fq.Fp4qError):
+            fq.fp4q_attention_fp8(*args)
+        with pytest.raises(fq.Fp4qError):
+            fq.fp4q_attention_fp8(*args, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+        with pytest.raises(fq.Fp4qError):
+            fq.fp4q_attention_fp8(*args, workspace=torch.empty(n + 8, dtype=torch.uint8, device="cuda")[8:])
+    fq.fp4q_attention_fp8(*args, workspace=torch.empty(max(n, 1), dtype=torch.uint8, device="cuda"))
+
+
+def test_streams_and_repeats(fq):
+    """Two calls at once on two streams with a workspace each; the same call twice gives the same bits."""
+    rng = np.random.default_rng(21)
+    o, lse, q, dev, table, cu = run(fq, rng, [1, 1, 1], [5000, 700, 64], 64, 128, 1, 4)
+    args = (*dev, i32(table.tolist()), i32(cu), i32([5000, 700, 64]), 1, 5000)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for s in streams:
+        with torch.cuda.stream(s):
+            outs += [fq.attention_fp8(q, *args) for _ in range(4)]
+    torch.cuda.synchronize()
+    for a, b in outs:
+        assert torch.equal(a, o) and torch.equal(b, lse)
+
+
+@pytest.mark.parametrize("new", [1, 33])
+def test_decoding_steps_in_a_graph(fq, new):
+    """Append and attend inside a graph captured once for the largest lengths, replayed as the sequences grow; two
+    graphs that share one workspace, replayed in turn on one stream."""
+    rng = np.random.default_rng(22)
+    page, D, heads, G, B, pool = 32, 128, 2, 2, 2, 40
+    cache = [np.zeros((pool, heads, page, D), np.uint8) for _ in range(2)] + [np.zeros((pool, heads), np.float32) for _ in range(2)]
+    dev = up(cache)
+    table = rng.permutation(pool)[:36].reshape(2, 18).astype(np.int32)
+    T = B * new
+    q, k, v = bf16(rng, T, heads * G, D), bf16(rng, T, heads, D), bf16(rng, T, heads, D)
+    tab, cu, lens = i32(table.tolist()), i32([0, new, T]), i32([new, new])
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    most = 18 * page
+    ws = fq.attention_fp8_workspace(q, dev[0], B, new, most)
+
+    def step():
+        fq.fp4q_kv_append_fp8(k, v, *dev, tab, cu, lens, new)
+        fq.fp4q_attention_fp8(q, *dev, tab, cu, lens, new, most, o, lse, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            step()
+    for t in dev:
+        t.zero_()
+    length = np.array([0, 0])
+    for turn in range(6):
+        for x, n in ((q, heads * G), (k, heads), (v, heads)):
+            x.copy_(bf16(rng, T, n, D))
+        length = length + new
+        lens.copy_(i32(length.tolist()))
+        graphs[turn % 2].replay()
+        torch.cuda.synchronize()
+        cache = fp8.kv_append(host(k), host(v), cache, table, [0, new, T], length)
+        for got, w in zip(dev, cache):
+            assert np.array_equal(to_np(got), w)
+        compare(o, lse, q, cache, table, [0, new, T], length, True, D ** -0.5)
+
+
+def test_a_layer_of_all_of_them(fq):
+    """The run that a served layer makes: an 8-bit projection to q, k, v, the cache's append, attention over it, and
+    the 8-bit output projection; each link against the oracle of that link's own inputs."""
+    rng = np.random.default_rng(23)
+    heads, G, D, page, hidden = 2, 4, 64, 16, 512
+    Hq = heads * G
+    qkv_w = fq.quantize_fp8(bf16(rng, (Hq + 2 * heads) * D, hidden, gain=hidden ** -0.5), fq.FP4Q_FP8_TILE)
+    out_w = fq.quantize_fp8(bf16(rng, hidden, Hq * D, gain=(Hq * D) ** -0.5), fq.FP4Q_FP8_TILE)
+    cache = [np.zeros((9, heads, page, D), np.uint8) for _ in range(2)] + [np.zeros((9, heads), np.float32) for _ in range(2)]
+    dev = up(cache)
+    table = np.array([[3, 1, 8, 5], [0, 2, 7, 6]], np.int32)
+    length = np.array([0, 0])
+    for new in ([20, 33], [1, 1], [1, 1], [5, 3]):
+        length = length + np.array(new)
+        T = sum(new)
+        x = bf16(rng, T, hidden)
+        xq = fq.quantize_fp8(x)
+        qkv = fq.gemm_fp8(*xq, *qkv_w).view(T, Hq + 2 * heads, D)
+        q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + heads], qkv[:, Hq + heads:]
+        args = (i32(table.tolist()), i32(cum(new)), i32(length.tolist()))
+        fq.kv_append_fp8(k, v, *dev, *args, max(new))
+        o, lse = fq.attention_fp8(q, *dev, *args, max(new), int(length.max()))
+        oq = fq.quantize_fp8(o.reshape(T, Hq * D))
+        y = fq.gemm_fp8(*oq, *out_w, out_dtype=torch.float32)
+        cache = fp8.kv_append(host(k.contiguous()), host(v.contiguous()), cache, table, cum(new), length)
+        for got, w in zip(dev, cache):
+            assert np.array_equal(to_np(got), w)
+        compare(o, lse, q.contiguous(), cache, table, cum(new), length, True, D ** -0.5)
+        codes, scales = fp8.quantize(host(o).reshape(T, Hq * D), False)
+        assert np.array_equal(to_np(oq[0]), codes) and np.array_equal(to_np(oq[1]), scales)
+        want, total = fp8.gemm(fp8.values(codes, scales, False), fp8.values(to_np(out_w[0]), to_np(out_w[1]), True))
+        assert (np.abs(to_np(y.double()) - want) <= (Hq * D + 16) * 2.0 ** -23 * total + 1e-30).all()
