@@ -45,6 +45,95 @@ fp4q_status check_fp8(const void* codes, int64_t rows, int64_t cols, int64_t ld,
     return FP4Q_OK;
 }
 
+// Codes [rows, K] with row stride ld, boxes of 128 columns x box_rows with the
+// 128-byte swizzle; columns past K and rows past `rows` read as zero codes.
+fp4q_status make_f8_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, int64_t ld, uint32_t box_rows) {
+    EncodeTiledFn enc;
+    fp4q_status st = encode_fn(&enc);
+    if (st != FP4Q_OK) return st;
+    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld};
+    cuuint32_t box[2] = {(cuuint32_t)kFp8Block, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FP4Q_OK : FP4Q_ERR_CUDA;
+}
+
+// The wide kernel's output [M, N], stored in boxes of 128 bytes x 32 rows.
+fp4q_status make_f8_out_map(CUtensorMap* map, void* d, int64_t M, int64_t N, int64_t ldd, int bf16) {
+    EncodeTiledFn enc;
+    fp4q_status st = encode_fn(&enc);
+    if (st != FP4Q_OK) return st;
+    const int64_t es = bf16 ? 2 : 4;
+    cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+    cuuint64_t strides[1] = {(cuuint64_t)(ldd * es)};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32u};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, d, dims, strides,
+                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FP4Q_OK : FP4Q_ERR_CUDA;
+}
+
+struct Fp8Operand {
+    const uint8_t* codes;
+    int64_t rows, ld;
+    const float* scales;
+    int64_t lds;
+    int tile;
+};
+
+// fp8_gemm_kernel<NT, VEC> with l's rows as lanes and c's as columns (NT = 256:
+// l = A; else l = B, its K blocks split over up to kF8MaxSplit CTAs while SMs
+// are free).
+template <int NT, bool VEC>
+fp4q_status launch_f8(const Fp8Operand& l, const Fp8Operand& c, int64_t K, Fp8GemmParams p, int sms, cudaStream_t s) {
+    using G = F8Geo<NT>;
+    auto kern = fp8_gemm_kernel<NT, VEC>;
+    static std::atomic<uint64_t> done{0};
+    fp4q_status st = ensure_smem(kern, G::smem, done);
+    if (st != FP4Q_OK) return st;
+    p.RL = l.rows;
+    p.RC = c.rows;
+    p.n_lt = spans(l.rows, kF8Lanes);
+    p.n_tiles = p.n_lt * spans(c.rows, NT);
+    if (p.n_tiles >= kMaxDim / kF8MaxSplit) return FP4Q_ERR_UNSUPPORTED;
+    p.sl = l.scales;
+    p.ldsl = l.lds;
+    p.l_tile = l.tile;
+    p.sc = c.scales;
+    p.ldsc = c.lds;
+    CUtensorMap map_l, map_c, map_d;
+    if ((st = make_f8_map(&map_l, l.codes, l.rows, K, l.ld, kF8Lanes)) != FP4Q_OK) return st;
+    if ((st = make_f8_map(&map_c, c.codes, c.rows, K, c.ld, NT)) != FP4Q_OK) return st;
+    map_d = map_l;  // a placeholder where no TMA store is made
+    int64_t grid;
+    if constexpr (G::wide) {
+        p.tma_store = p.ldd * (p.out_bf16 ? 2 : 4) % 16 == 0;
+        if (p.tma_store && (st = make_f8_out_map(&map_d, p.d, l.rows, c.rows, p.ldd, p.out_bf16)) != FP4Q_OK) return st;
+        grid = std::min<int64_t>(p.n_tiles, sms);
+    } else {
+        p.split = (int32_t)std::max<int64_t>(1, std::min<int64_t>({(int64_t)kF8MaxSplit, (int64_t)p.n_kb, sms / p.n_tiles}));
+        grid = p.n_tiles * p.split;
+    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)G::threads);
+    cfg.dynamicSmemBytes = (size_t)G::smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, map_l, map_c, map_d, p) == cudaSuccess ? FP4Q_OK : FP4Q_ERR_CUDA;
+}
+
 fp4q_status check_cache(const fp4q_kv_cache* c, KvCacheView* v) {
     if (!c) return FP4Q_ERR_INVALID_ARG;
     if (c->num_pages < 0 || c->num_kv_heads <= 0 || c->table_stride < 0 || c->page_size <= 0 || c->head_dim <= 0)
@@ -134,26 +223,26 @@ FP4Q_API fp4q_status fp4q_gemm_fp8(const uint8_t* a_codes, int64_t lda, const fl
     if ((st = check_fp8(b_codes, N, K, ldb, b_scales, ldbs, b_block)) != FP4Q_OK) return st;
     if (!d) return FP4Q_ERR_INVALID_ARG;
     if (!aligned(d, 16)) return FP4Q_ERR_ALIGNMENT;
+    int sms = 0;
+    if ((st = sm_count(&sms)) != FP4Q_OK) return st;
+    Fp8Operand a{a_codes, M, lda, a_scales, ldas, 0}, b{b_codes, N, ldb, b_scales, ldbs, b_block == FP4Q_FP8_TILE};
     Fp8GemmParams p{};
-    p.a = a_codes;
-    p.b = b_codes;
-    p.sa = a_scales;
-    p.sb = b_scales;
-    p.lda = lda;
-    p.ldb = ldb;
-    p.ldas = ldas;
-    p.ldbs = ldbs;
-    p.M = M;
-    p.N = N;
-    p.K = K;
+    p.n_kb = (int32_t)spans(K, kFp8Block);
     p.d = d;
     p.ldd = ldd;
     p.out_bf16 = d_bf16;
-    p.b_tile = b_block == FP4Q_FP8_TILE;
-    p.n_nt = spans(N, kFp8SimpleTile);
-    const int64_t tiles = spans(M, kFp8SimpleTile) * p.n_nt;
-    if (tiles >= kMaxDim) return FP4Q_ERR_UNSUPPORTED;
-    return launch(fp8_gemm_simple_kernel, (int)tiles, 256, 0, (cudaStream_t)stream, p);
+    p.split = 1;
+    // The wide kernel has a tile for at least half of the SMs, or A's rows fill
+    // no narrow tile's columns.
+    const int64_t wide_tiles = spans(M, kF8Lanes) * spans(N, 256);
+    if (M > 128 && 2 * wide_tiles > sms) {
+        if (b.tile) return launch_f8<256, false>(a, b, K, p, sms, (cudaStream_t)stream);
+        return launch_f8<256, true>(a, b, K, p, sms, (cudaStream_t)stream);
+    }
+    if (M <= 16) return launch_f8<16, true>(b, a, K, p, sms, (cudaStream_t)stream);
+    if (M <= 32) return launch_f8<32, true>(b, a, K, p, sms, (cudaStream_t)stream);
+    if (M <= 64) return launch_f8<64, true>(b, a, K, p, sms, (cudaStream_t)stream);
+    return launch_f8<128, true>(b, a, K, p, sms, (cudaStream_t)stream);
 }
 
 FP4Q_API fp4q_status fp4q_kv_append_fp8(const void* k, int64_t ldk, const void* v, int64_t ldv, int64_t tokens,

@@ -1,62 +1,437 @@
-// fp4q_fp8_gemm.cuh -- D = A B^T of E4M3 codes under block-128 scales:
+// fp4q_fp8_gemm.cuh -- D = A B^T of E4M3 codes under block-128 scales, on the
+// 5th-generation tensor cores (tcgen05, kind::f8f6f4):
+//
 //   D[m, n] = sum_kb SA[kb, m] SB[kb, n] sum_{k in kb} A[m, k] B[n, k]
+//
+// The inner sum of one block is four MMAs (K = 32 each) into fp32 in tensor
+// memory; the scales differ per row and block and are no power of two, so each
+// block's sum is read back, scaled and added in fp32 registers.  Two TMEM
+// buffers let the MMAs of block kb + 1 run under that.
+//
+// One operand's rows are the 128 TMEM lanes (a thread = a row), the other's are
+// the accumulator's columns:
+//   wide kernel    lanes = rows of A, 256 columns = rows of B; persistent;
+//   narrow kernel  lanes = rows of B (the weights), 16..128 columns = rows of
+//                  A: few rows of A do not waste lanes, and the K blocks of a
+//                  tile are split over a cluster of CTAs whose partial sums
+//                  are added through distributed shared memory in rank order.
+//
+// CTA roles: warp 0 lane 0 streams the K blocks of both operands by TMA into a
+// ring; warp 1 allocates TMEM, lane 0 issues the MMAs; the other warps (one
+// group of four per 128 columns) scale and accumulate, then store.
+// Every wait is bounded; a wait that runs out sets g_device_error and the role
+// stops; the CTA drains its copies and MMAs and frees TMEM before it exits.
 #pragma once
 
 #include "fp4q_fp8.cuh"
+#include "fp4q_mma.cuh"
 
 namespace fp4q {
 
+constexpr int kF8Lanes = 128;
+constexpr int kF8MaxSplit = 8;                      // CTAs of a portable cluster
+constexpr int kF8LaneBytes = kF8Lanes * kFp8Block;  // 16 KiB of the lane operand per K block
+
 struct Fp8GemmParams {
-    const uint8_t *a, *b;
-    const float *sa, *sb;
-    int64_t lda, ldb, ldas, ldbs;
-    int64_t M, N, K;
+    int64_t RL, RC;          // rows of the lane and the column operand
+    int32_t n_kb;            // K blocks
+    int64_t n_lt, n_tiles;   // lane tiles; tiles (lane tile fastest)
+    const float *sl, *sc;    // scales [n_kb, ld]
+    int64_t ldsl, ldsc;
+    int32_t l_tile;          // the lane operand's scales are per 128 x 128 tile
     void* d;
     int64_t ldd;
-    int out_bf16, b_tile;
-    int64_t n_nt;
+    int32_t out_bf16;
+    int32_t tma_store;       // wide kernel: D's rows are 16 bytes apart in step
+    int32_t split;           // narrow kernel: CTAs of the cluster that share a tile's K blocks
 };
 
-constexpr int kFp8SimpleTile = 64;
-__global__ void __launch_bounds__(256) fp8_gemm_simple_kernel(const Fp8GemmParams p) {
-    __shared__ float as[32][kFp8SimpleTile + 1], bs[32][kFp8SimpleTile + 1];
+// kind::f8f6f4 instruction descriptor: D fp32 (1 at [4,6)), A and B E4M3 (0 at
+// [7,10), [10,13)), both K-major, N >> 3 at [17,23), M >> 4 at [24,29).
+__host__ __device__ constexpr uint32_t f8_idesc(int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kF8Lanes >> 4) << 24);
+}
+
+// D[tmem] (+)= A * B^T, E4M3 operands, M = 128, K = 32.
+__device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 16 consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The float at shared-memory address `saddr` of the cluster's CTA `rank`.
+__device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// The wide kernel's register split: 384 threads start with 168 each; the first
+// warpgroup gives up 96 so that the two epilogue ones, which hold 128 sums per
+// thread, have 216 (72 + 2 * 216 = 3 * 168).
+constexpr int kF8RegsRoles = 72, kF8RegsEpilogue = 216;
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int NT>
+struct F8Geo {
+    static constexpr bool wide = NT == 256;
+    static constexpr int groups = wide ? 2 : 1;          // epilogue groups of four warps
+    static constexpr int cols = NT / groups;             // accumulator columns of a thread
+    static constexpr int first_epi = wide ? 4 : 2;       // first epilogue warp (wide: whole warpgroups, see kF8Regs)
+    static constexpr int threads = 32 * first_epi + 128 * groups;
+    static constexpr int stage_bytes = kF8LaneBytes + NT * kFp8Block;
+    static constexpr int stages = wide ? 4 : (192 * 1024) / stage_bytes;
+    static constexpr int ring = stages * stage_bytes;
+    static constexpr int stg_off = ring;                 // wide: 4 KiB of output staging per epilogue warp
+    static constexpr int sc_off = stg_off + (wide ? 8 * 4096 : 0);  // column scales, two buffers per group
+    static constexpr int bar_off = sc_off + groups * 2 * cols * 4;
+    static constexpr int num_bars = 2 * stages + 5;
+    static constexpr int slot_off = bar_off + num_bars * 8;
+    static constexpr int smem = 896 + slot_off + 16;     // the base is 128-byte aligned, the ring 1024
+    static constexpr uint32_t tmem_cols = 2 * NT;        // two buffers
+    static_assert(stage_bytes % 1024 == 0, "stages keep the 1024-byte alignment of the swizzle");
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static_assert(wide || ring >= cols * kF8Lanes * 4, "the ring holds the partial sums of the split");
+};
+
+// One element of D.
+__device__ __forceinline__ void f8_store(const Fp8GemmParams& p, int64_t m, int64_t n, float v) {
+    if (p.out_bf16)
+        static_cast<uint16_t*>(p.d)[m * p.ldd + n] = (uint16_t)bf16x2_pack(v, 0.0f);
+    else
+        static_cast<float*>(p.d)[m * p.ldd + n] = v;
+}
+
+// acc += scale * (one K block's sums), columns [0, C) of TMEM at taddr.  VEC:
+// column scales from shared memory (broadcast reads), else f covers both scales.
+template <int C, bool VEC>
+__device__ __forceinline__ void f8_accumulate(uint32_t taddr, float f, const float* sc, float (&acc)[C]) {
+    constexpr int W = C < 32 ? 16 : 32;
+#pragma unroll
+    for (int c0 = 0; c0 < C; c0 += W) {
+        float v[W];
+        if constexpr (W == 32)
+            tmem_ld32(taddr + c0, v);
+        else
+            tmem_ld16(taddr + c0, v);
+#pragma unroll
+        for (int c = 0; c < W; c += 4) {
+            if constexpr (VEC) {
+                const float4 s = *reinterpret_cast<const float4*>(sc + c0 + c);
+                acc[c0 + c] = fmaf(v[c] * f, s.x, acc[c0 + c]);
+                acc[c0 + c + 1] = fmaf(v[c + 1] * f, s.y, acc[c0 + c + 1]);
+                acc[c0 + c + 2] = fmaf(v[c + 2] * f, s.z, acc[c0 + c + 2]);
+                acc[c0 + c + 3] = fmaf(v[c + 3] * f, s.w, acc[c0 + c + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[c0 + c + i] = fmaf(v[c + i], f, acc[c0 + c + i]);
+            }
+        }
+    }
+}
+
+// VEC: the column operand's scales are per row (the narrow kernel's always are).
+template <int NT, bool VEC>
+__global__ void __launch_bounds__(F8Geo<NT>::threads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_l, const __grid_constant__ CUtensorMap map_c,
+                    const __grid_constant__ CUtensorMap map_d, const Fp8GemmParams p) {
+    using G = F8Geo<NT>;
+    constexpr int S = G::stages, C = G::cols;
+    static_assert(VEC || G::wide, "the narrow kernel's columns are rows of A");
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = align_shared<1024>(smem_raw);
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t full0 = smem_u32(smem + G::bar_off), empty0 = full0 + 8 * S;
+    const uint32_t accf = empty0 + 8 * S, acce = accf + 16, done_bar = acce + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::slot_off);
+
+    if (tid == 0) {
+        prefetch_tmap(&map_l);
+        prefetch_tmap(&map_c);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(accf + 8 * i, 1);
+            mbar_init(acce + 8 * i, 4 * G::groups);  // one arrival per epilogue warp
+        }
+        mbar_init(done_bar, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), G::tmem_cols);
+        tmem_relinquish();
+    }
     pdl_wait();
     pdl_trigger();
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t m0 = (int64_t)(blockIdx.x / p.n_nt) * kFp8SimpleTile, n0 = (int64_t)(blockIdx.x % p.n_nt) * kFp8SimpleTile;
-    float acc[4][4] = {};
-    for (int64_t kb = 0; kb * kFp8Block < p.K; ++kb) {
-        float sum[4][4] = {};
-        for (int k0 = 0; k0 < kFp8Block; k0 += 32) {
-            for (int e = threadIdx.x; e < kFp8SimpleTile * 32; e += 256) {
-                const int r = e >> 5, k = e & 31;
-                const int64_t kk = kb * kFp8Block + k0 + k;
-                as[k][r] = m0 + r < p.M && kk < p.K ? e4m3_decode(p.a[(m0 + r) * p.lda + kk]) : 0.0f;
-                bs[k][r] = n0 + r < p.N && kk < p.K ? e4m3_decode(p.b[(n0 + r) * p.ldb + kk]) : 0.0f;
-            }
-            __syncthreads();
-            for (int k = 0; k < 32; ++k)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(as[k][ty + 16 * i], bs[k][tx + 16 * j], sum[i][j]);
-            __syncthreads();
-        }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-                if (m < p.M && n < p.N)
-                    acc[i][j] = fmaf(sum[i][j], p.sa[kb * p.ldas + m] * p.sb[kb * p.ldbs + (p.b_tile ? n / kFp8Block : n)],
-                                     acc[i][j]);
-            }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    // this CTA's tiles (the narrow kernel has one) and K blocks
+    const int64_t unit = G::wide ? (int64_t)blockIdx.x : (int64_t)blockIdx.x / p.split;
+    const int64_t step = G::wide ? (int64_t)gridDim.x : p.n_tiles;
+    const uint32_t rank = G::wide ? 0u : cluster_rank();
+    const int kb0 = G::wide ? 0 : (int)((int64_t)p.n_kb * rank / p.split);
+    const int kbs = (G::wide ? p.n_kb : (int)((int64_t)p.n_kb * (rank + 1) / p.split)) - kb0;
+    const int64_t n_my = p.n_tiles > unit ? (p.n_tiles - 1 - unit) / step + 1 : 0;
+
+    const int epi = (int)warp - G::first_epi;
+    const uint32_t quarter = warp & 3;  // the TMEM lanes a warp may read
+    const int grp = epi >> 2;
+
+    if (epi < 0) {
+        if constexpr (G::wide) reg_dec<kF8RegsRoles>();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m >= p.M || n >= p.N) continue;
-            if (p.out_bf16)
-                static_cast<uint16_t*>(p.d)[m * p.ldd + n] = (uint16_t)bf16x2_pack(acc[i][j], 0.0f);
-            else
-                static_cast<float*>(p.d)[m * p.ldd + n] = acc[i][j];
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const int64_t total = n_my * kbs;
+            int64_t g = 0;
+            int s = 0, kb = 0;
+            uint32_t ph = 1;
+            int64_t t = unit;
+            for (; g < total; ++g) {
+                if (g >= S && !mbar_wait(empty0 + 8 * s, ph)) {
+                    atomicOr(&g_device_error, kErrWaitTimeout);
+                    break;
+                }
+                const int64_t lt = t % p.n_lt, ct = t / p.n_lt;
+                uint8_t* st = smem + s * G::stage_bytes;
+                const uint32_t bar = full0 + 8 * s;
+                mbar_arrive_expect_tx(bar, G::stage_bytes);
+                tma_load_2d(smem_u32(st), &map_l, (kb0 + kb) * kFp8Block, (int32_t)(lt * kF8Lanes), bar);
+                tma_load_2d(smem_u32(st + kF8LaneBytes), &map_c, (kb0 + kb) * kFp8Block, (int32_t)(ct * NT), bar);
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                if (++kb == kbs) {
+                    kb = 0;
+                    t += step;
+                }
+            }
+            // every issued copy lands before the CTA may exit
+            for (int64_t k = (g > S ? g - S : 0); k < g; ++k)
+                (void)mbar_wait(full0 + 8 * (int)(k % S), (uint32_t)((k / S) & 1));
         }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            bool ok = true;
+            const int64_t total = n_my * kbs;
+            int s = 0;
+            uint32_t ph = 0;
+            for (int64_t g = 0; g < total; ++g) {
+                const int buf = (int)(g & 1);
+                if (!mbar_wait(full0 + 8 * s, ph) ||
+                    (g >= 2 && !mbar_wait(acce + 8 * buf, (uint32_t)(((g >> 1) - 1) & 1)))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * G::stage_bytes);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    umma_f8(tmem_base + NT * buf, sw128_desc(st + 32 * j), sw128_desc(st + kF8LaneBytes + 32 * j),
+                            f8_idesc(NT), j > 0 ? 1u : 0u);
+                tc_commit(empty0 + 8 * s);
+                tc_commit(accf + 8 * buf);
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            if (!ok) atomicOr(&g_device_error, kErrWaitTimeout);
+            // all MMAs of this CTA complete before TMEM is freed
+            tc_commit(done_bar);
+            if (!mbar_wait(done_bar, 0)) atomicOr(&g_device_error, kErrWaitTimeout);
+        }
+    } else if (epi >= 0) {
+        // ------------------------------------------------ scale, accumulate, store
+        if constexpr (G::wide) reg_inc<kF8RegsEpilogue>();
+        float acc[C];
+        const int t = (int)quarter * 32 + (int)lane;  // TMEM lane, also this thread's place in the group
+        const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + (uint32_t)(grp * C);
+        float* sc_buf = reinterpret_cast<float*>(smem + G::sc_off) + grp * 2 * C;
+        const int stg = epi * 4096;
+        int64_t g = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int64_t i = 0; i < n_my; ++i) {
+            const int64_t tile = unit + i * step;
+            const int64_t lt = tile % p.n_lt, ct = tile / p.n_lt;
+            const int64_t row = lt * kF8Lanes + t, c0 = ct * NT + grp * C;
+            // scale addresses, clamped to rows that exist (the others' results are dropped)
+            const float* sl = p.sl + (int64_t)kb0 * p.ldsl + (p.l_tile ? lt : min64(row, p.RL - 1));
+            const float* sc = p.sc + (int64_t)kb0 * p.ldsc + (VEC ? min64(c0 + (t < C ? t : 0), p.RC - 1) : min64(c0, p.RC - 1) / kFp8Block);
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+            // scales two blocks ahead of their use
+            float l0 = __ldg(sl), s0 = __ldg(sc), l1 = 0.0f, s1 = 0.0f;
+            if (kbs > 1) {
+                l1 = __ldg(sl + p.ldsl);
+                s1 = __ldg(sc + p.ldsc);
+            }
+#pragma unroll 1
+            for (int kb = 0; kb < kbs; ++kb, ++g) {
+                float l2 = 0.0f, s2 = 0.0f;
+                if (kb + 2 < kbs) {
+                    l2 = __ldg(sl + (int64_t)(kb + 2) * p.ldsl);
+                    s2 = __ldg(sc + (int64_t)(kb + 2) * p.ldsc);
+                }
+                const int buf = (int)(g & 1);
+                if constexpr (VEC) {
+                    if (t < C) sc_buf[buf * C + t] = s0;
+                    bar_sync(1 + grp, 128);
+                }
+                if (ok) {  // once a wait has run out, the rest is skipped
+                    ok = __all_sync(0xffffffffu, mbar_wait(accf + 8 * buf, (uint32_t)((g >> 1) & 1)));
+                    if (!ok && lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
+                }
+                tc_fence_after();
+                if (ok) f8_accumulate<C, VEC>(taddr + NT * buf, VEC ? l0 : l0 * s0, sc_buf + buf * C, acc);
+                // this warp's reads of the buffer are done
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acce + 8 * buf);
+                l0 = l1;
+                l1 = l2;
+                s0 = s1;
+                s1 = s2;
+            }
+            if constexpr (G::wide) {
+                if (p.tma_store) {
+                    // 32 rows x 128 bytes at a time through this warp's 4 KiB (128-byte swizzle)
+                    const uint32_t buf32 = smem_u32(smem + G::stg_off + stg);
+#pragma unroll
+                    for (int h = 0; h < C / 32; ++h) {  // boxes of 32 fp32 columns, or halves of 64 bf16 ones
+                        const bool first = !p.out_bf16 || (h & 1) == 0, last = !p.out_bf16 || (h & 1) == 1;
+                        if (first) {
+                            if (lane == 0) bulk_wait_read0();
+                            __syncwarp();
+                        }
+                        if (p.out_bf16) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                sts_v4(buf32 + swz128(lane, 64 * (h & 1) + 16 * q),
+                                       bf16x2_pack(acc[32 * h + 8 * q], acc[32 * h + 8 * q + 1]),
+                                       bf16x2_pack(acc[32 * h + 8 * q + 2], acc[32 * h + 8 * q + 3]),
+                                       bf16x2_pack(acc[32 * h + 8 * q + 4], acc[32 * h + 8 * q + 5]),
+                                       bf16x2_pack(acc[32 * h + 8 * q + 6], acc[32 * h + 8 * q + 7]));
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                sts_v4(buf32 + swz128(lane, 16 * q), __float_as_uint(acc[32 * h + 4 * q]),
+                                       __float_as_uint(acc[32 * h + 4 * q + 1]), __float_as_uint(acc[32 * h + 4 * q + 2]),
+                                       __float_as_uint(acc[32 * h + 4 * q + 3]));
+                        }
+                        if (last) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            const int64_t col = c0 + 32 * h - (p.out_bf16 ? 32 : 0), r0 = lt * kF8Lanes + quarter * 32;
+                            if (lane == 0 && col < p.RC && r0 < p.RL) {
+                                tma_store_2d(&map_d, (int32_t)col, (int32_t)r0, buf32);
+                                bulk_commit();
+                            }
+                        }
+                    }
+                } else if (row < p.RL) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        if (c0 + c < p.RC) f8_store(p, row, c0 + c, acc[c]);
+                }
+            } else {
+                if (p.split == 1) {
+                    // lanes are consecutive columns of D: a warp writes runs of 32
+                    if (row < p.RL) {
+#pragma unroll
+                        for (int c = 0; c < C; ++c)
+                            if (c0 + c < p.RC) f8_store(p, c0 + c, row, acc[c]);
+                    }
+                } else {
+                    // every block of this CTA has been read: the ring holds its partial sums now
+                    float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) part[c * kF8Lanes + t] = acc[c];
+                }
+            }
+        }
+        if constexpr (G::wide) {
+            if (lane == 0) bulk_wait0();
+        }
+    }
+
+    if constexpr (!G::wide) {
+        if (p.split > 1) {
+            __syncthreads();
+            cluster_sync();
+            // rank r adds columns r, r + split, ... of the tile, rank 0's part first
+            if (epi >= 0) {
+                const int t = (int)quarter * 32 + (int)lane;
+                const int64_t row = (unit % p.n_lt) * kF8Lanes + t, c0 = unit / p.n_lt * NT;
+                const uint32_t part = smem_u32(smem) + 4 * t;
+                for (int c = (int)rank; c < C && c0 + c < p.RC; c += p.split) {
+                    float v[kF8MaxSplit];
+#pragma unroll
+                    for (int r = 0; r < kF8MaxSplit; ++r)
+                        v[r] = r < p.split ? ld_cluster(part + c * kF8Lanes * 4, r) : 0.0f;
+#pragma unroll
+                    for (int r = 1; r < kF8MaxSplit; ++r) v[0] += v[r];
+                    if (row < p.RL) f8_store(p, c0 + c, row, v[0]);
+                }
+            }
+            cluster_sync();  // no CTA leaves while another reads its sums
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, G::tmem_cols);
+    }
 }
 
 }  // namespace fp4q
