@@ -308,22 +308,12 @@ __global__ void __launch_bounds__(F8Geo<NT>::threads, 1)
             const float* sc = p.sc + (int64_t)kb0 * p.ldsc + (VEC ? min64(c0 + (t < C ? t : 0), p.RC - 1) : min64(c0, p.RC - 1) / kFp8Block);
 #pragma unroll
             for (int c = 0; c < C; ++c) acc[c] = 0.0f;
-            // scales two blocks ahead of their use
-            float l0 = __ldg(sl), s0 = __ldg(sc), l1 = 0.0f, s1 = 0.0f;
-            if (kbs > 1) {
-                l1 = __ldg(sl + p.ldsl);
-                s1 = __ldg(sc + p.ldsc);
-            }
-#pragma unroll 1
-            for (int kb = 0; kb < kbs; ++kb, ++g) {
-                float l2 = 0.0f, s2 = 0.0f;
-                if (kb + 2 < kbs) {
-                    l2 = __ldg(sl + (int64_t)(kb + 2) * p.ldsl);
-                    s2 = __ldg(sc + (int64_t)(kb + 2) * p.ldsc);
-                }
+            auto lane_scale = [&](int kb) { return __ldg(sl + min(kb, kbs - 1) * p.ldsl); };
+            auto col_scale = [&](int kb) { return __ldg(sc + min(kb, kbs - 1) * p.ldsc); };
+            auto block = [&](float l, float s) {
                 const int buf = (int)(g & 1);
                 if constexpr (VEC) {
-                    if (t < C) sc_buf[buf * C + t] = s0;
+                    if (t < C) sc_buf[buf * C + t] = s;
                     bar_sync(1 + grp, 128);
                 }
                 if (ok) {  // once a wait has run out, the rest is skipped
@@ -331,15 +321,25 @@ __global__ void __launch_bounds__(F8Geo<NT>::threads, 1)
                     if (!ok && lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
                 }
                 tc_fence_after();
-                if (ok) f8_accumulate<C, VEC>(taddr + NT * buf, VEC ? l0 : l0 * s0, sc_buf + buf * C, acc);
+                if (ok) f8_accumulate<C, VEC>(taddr + NT * buf, VEC ? l : l * s, sc_buf + buf * C, acc);
                 // this warp's reads of the buffer are done
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(acce + 8 * buf);
-                l0 = l1;
-                l1 = l2;
-                s0 = s1;
-                s1 = s2;
+                ++g;
+            };
+            // two blocks a turn: the next two's scales are on their way meanwhile,
+            // and nothing waits for them (moving them along each block would)
+            float l0 = lane_scale(0), l1 = lane_scale(1), s0 = col_scale(0), s1 = col_scale(1);
+#pragma unroll 1
+            for (int kb = 0; kb < kbs; kb += 2) {
+                const float m0 = lane_scale(kb + 2), m1 = lane_scale(kb + 3), t0 = col_scale(kb + 2), t1 = col_scale(kb + 3);
+                block(l0, s0);
+                if (kb + 1 < kbs) block(l1, s1);
+                l0 = m0;
+                l1 = m1;
+                s0 = t0;
+                s1 = t1;
             }
             if constexpr (G::wide) {
                 if (p.tma_store) {
