@@ -1,4 +1,6 @@
-// fp4q_attn.cuh -- attention of bf16 queries over the paged 8-bit cache.
+// fp4q_attn.cuh -- attention of bf16 queries over the paged 8-bit cache,
+//   o = softmax(scale q K^T) V,  lse = ln sum exp(scale q K^T),
+// K and V = E4M3 code * the page's scale.
 #pragma once
 
 #include "fp4q_kv.cuh"
@@ -52,51 +54,430 @@ __device__ __forceinline__ int64_t attn_page(const AttnParams& p, int64_t b, int
     return id;
 }
 
-// One warp per (query, head); lanes share the head dimension.
+// ------------------------------------------------------------------ few queries
+//
+// One CTA: one sequence, one K/V head, 16 rows (query i, head g of the group:
+// row i * G + g) and one run of keys; four warps take turns of 16 keys, which
+// lie within one page.  Decoding is bound by reading the cache, so the codes go
+// from global memory straight into the registers that the tensor cores read,
+// each lane loading whole 16-byte pieces: which of a product's k (or n) indices
+// a lane's bytes stand for is free as long as both operands agree.
+//   S = Q K^T: lane (g, t) = (lane / 4, lane % 4) holds dims D/4 t .. of key g
+//     (and 8 + g); its next four bytes are the k indices 2t, 2t+1, 2t+8, 2t+9
+//     of the next m16n8k16 step.
+//   O = P V: the lane's keys are 2t, 2t+1, 2t+8, 2t+9 (as S leaves them) and its
+//     dims D/8 g ..; byte j of each makes column g of output tile j, dim D/8 g + j.
+// E4M3 values are exact in fp16, and so is a bf16 query scaled by a power of
+// two to a row maximum of 2^14 (dims 2^-28 below it lose bits).
+//
+// Softmax, one pass: with the page's V scale vs, the weights enter P V as
+// w = exp2(s + log2 vs - m) 2^14 <= 2^14, m the running maximum of s + log2 vs,
+// in fp16: full precision whatever the V scales are, and down to 2^-28 of the
+// largest before fp16's subnormals.  The denominator sums w / vs in fp32.
+
+constexpr float kAttnWeightLog2 = 14.0f;
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t f16x2_pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_stream8(const uint8_t* p) {
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// What one split leaves for the others: rows of D sums, then the row's maximum
+// and denominator, in the workspace (one slot per row of a row tile and split).
 template <int D>
-__global__ void __launch_bounds__(128) attn_simple_kernel(const AttnParams p) {
-    constexpr int N = D / 32;
+constexpr int kAttnSlot = D + 2;
+
+constexpr int kAttnRows = 16, kAttnStep = 16;
+constexpr int kAttnMaxChunk = 16384;  // keys of one split: its pages' ids and scales are in shared memory
+
+struct AttnSplit {
+    int64_t row_tiles, splits;
+    int64_t chunk;      // keys per split, a multiple of 128
+    int32_t slot_rows;  // rows of a tile that may exist: min(16, max_q * G)
+    float* ws;          // NULL: one split
+};
+
+// Smallest v such that keys >= v of the row are masked.
+__device__ __forceinline__ int attn_limit(const AttnParams& p, const AttnSeq& s, int64_t r) {
+    const int64_t i = r / p.group;
+    const int64_t lim = p.causal ? s.len - s.n + i + 1 : s.len;
+    return i < s.n && lim > 0 ? (int)lim : 0;
+}
+
+template <int D>
+constexpr int kAttnWarps = D == 256 ? 2 : 4;  // (the sums of four would not fit in 48 KiB)
+
+template <int D>
+struct AttnFrag {
+    static constexpr int kw = D / 16;  // words of a lane's part of one key of K: D/4 bytes
+    static constexpr int vw = D / 32;  // words of a lane's part of one key of V: D/8 bytes
+    uint32_t k[2][kw], v[4][vw];
+};
+
+template <int D>
+__device__ __forceinline__ void attn_load(AttnFrag<D>& f, const uint8_t* kp, const uint8_t* vp, int g, int t) {
+    // kp, vp: the step's first key of this head's page
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint8_t* src = kp + (g + 8 * i) * D + t * (D / 4);
+#pragma unroll
+        for (int w = 0; w < D / 16; w += 4) {
+            const uint4 x = ld_stream(src + 4 * w);
+            f.k[i][w] = x.x;
+            f.k[i][w + 1] = x.y;
+            f.k[i][w + 2] = x.z;
+            f.k[i][w + 3] = x.w;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint8_t* src = vp + (2 * t + (i & 1) + 8 * (i >> 1)) * D + g * (D / 8);
+        if constexpr (D == 64) {
+            const uint2 x = ld_stream8(src);
+            f.v[i][0] = x.x;
+            f.v[i][1] = x.y;
+        } else {
+#pragma unroll
+            for (int w = 0; w < D / 32; w += 4) {
+                const uint4 x = ld_stream(src + 4 * w);
+                f.v[i][w] = x.x;
+                f.v[i][w + 1] = x.y;
+                f.v[i][w + 2] = x.z;
+                f.v[i][w + 3] = x.w;
+            }
+        }
+    }
+}
+
+// Bytes of w that are NaN codes, as 0xff; the others 0.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
+template <int D>
+__global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const AttnParams p, const AttnSplit sp) {
+    constexpr int KW = D / 16, NJ = D / 8, kWarps = kAttnWarps<D>;
+    // row sums of the four warps; pages' ids and scales before
+    __shared__ __align__(16) float red[kWarps * kAttnRows * (D + 4)];
+    __shared__ float red_m[kWarps][kAttnRows], red_l[kWarps][kAttnRows];
+    static_assert(sizeof(red) >= 3 * 4 * kAttnMaxChunk / 16, "page ids and scales fit");
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    int64_t u = blockIdx.x;
+    const int64_t split = u % sp.splits;
+    u /= sp.splits;
+    const int64_t rt = u % sp.row_tiles;
+    u /= sp.row_tiles;
+    const int hk = (int)(u % p.c.heads);
+    const int64_t b = u / p.c.heads;
+    const AttnSeq s = attn_seq(p, b, threadIdx.x == 0);
+    const int64_t r0 = rt * kAttnRows;
+    const int64_t rows = min64(s.n * p.group - r0, kAttnRows);
+    if (rows <= 0) return;
+    // keys this tile sees (the last row sees most), and this split's part of them
+    const int64_t most = attn_limit(p, s, r0 + rows - 1);
+    const int64_t k0 = split * sp.chunk, k1 = min64(most, k0 + sp.chunk);
+    if (split > 0 && k0 >= k1) return;
+    const int64_t every = attn_limit(p, s, r0);  // keys below are seen by every row of the tile
+    const int lim0 = attn_limit(p, s, r0 + g), lim1 = attn_limit(p, s, r0 + g + 8);
+
+    // page ids and scales of the split
+    const int n_pages = k0 < k1 ? (int)((k1 - k0 + p.c.page - 1) / p.c.page) : 0;
+    int32_t* ids = reinterpret_cast<int32_t*>(red);
+    float *ks = red + kAttnMaxChunk / 16, *vs = ks + kAttnMaxChunk / 16;
+    for (int i = threadIdx.x; i < n_pages; i += 32 * kWarps) {
+        const int64_t at = attn_page(p, b, k0 / p.c.page + i, true) * p.c.heads + hk;
+        ids[i] = (int32_t)at;
+        ks[i] = p.c.k_scale[at] * p.scale_log2;
+        vs[i] = p.c.v_scale[at];
+    }
+
+    // this lane's part of the queries: rows g and g + 8, dims D/4 t .. D/4 t + D/4 - 1, scaled by a power of two
+    uint32_t qa[KW][4];
+    float qs[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t r = r0 + g + 8 * i;
+        const bool live = r < s.n * p.group;
+        const uint16_t* src = p.q + (s.first + (live ? r / p.group : 0)) * p.ldq + ((int64_t)hk * p.group + (live ? r % p.group : 0)) * D + t * (D / 4);
+        uint32_t w[D / 8];
+        float amax = 0.0f;
+#pragma unroll
+        for (int c = 0; c < D / 8; c += 4) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (live) x = __ldg(reinterpret_cast<const uint4*>(src + 2 * c));
+            w[c] = x.x;
+            w[c + 1] = x.y;
+            w[c + 2] = x.z;
+            w[c + 3] = x.w;
+            amax = fmaxf(amax, amax8(x));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // up = 2^(14 - floor(log2 amax)), as two factors (it may pass fp32's range); undone through qs
+        int e = 14 + 127 - (int)(__float_as_uint(fmaxf(amax, 0x1p-126f)) >> 23);
+        if (amax == 0.0f) e = 0;
+        const int e1 = e / 2, e2 = e - e1;
+        const float u1 = __int_as_float((127 + e1) << 23), u2 = __int_as_float((127 + e2) << 23);
+        qs[i] = __int_as_float((127 - e1) << 23) * __int_as_float((127 - e2) << 23);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+            const uint32_t h = f16x2_pack(bf16lo(w[c]) * u1 * u2, bf16hi(w[c]) * u1 * u2);
+            qa[c / 2][i + 2 * (c & 1)] = h;
+        }
+    }
+    __syncthreads();
+
+    float o[NJ][4];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+
+    const int64_t plane = (int64_t)p.c.page * D;
+    const int steps = k0 < k1 ? (int)((k1 - k0 + kAttnStep - 1) / kAttnStep) : 0;
+    const int per_page = p.c.page / kAttnStep, shift = per_page == 1 ? 0 : per_page == 2 ? 1 : per_page == 4 ? 2 : 3;
+    auto load = [&](AttnFrag<D>& f, int st) {
+        const int64_t at = ids[st >> shift] * plane + (int64_t)(st & (per_page - 1)) * kAttnStep * D;
+        attn_load<D>(f, p.c.k + at, p.c.v + at, g, t);
+    };
+    AttnFrag<D> cur;
+    if (warp < steps) load(cur, warp);
+#pragma unroll 1
+    for (int st = warp; st < steps; st += kWarps) {
+        AttnFrag<D> f = cur;
+        if (st + kWarps < steps) load(cur, st + kWarps);
+        const int page = st >> shift;
+        const int64_t key = k0 + (int64_t)st * kAttnStep;
+        const float kscale = ks[page], vscale = vs[page];
+
+        float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // keys 2t, 2t+1; 8 + 2t, ...
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+            mma_f16(s0, qa[w][0], qa[w][1], qa[w][2], qa[w][3], e4m3x2_f16x2(f.k[0][w]), e4m3x2_f16x2(f.k[0][w] >> 16));
+            mma_f16(s1, qa[w][0], qa[w][1], qa[w][2], qa[w][3], e4m3x2_f16x2(f.k[1][w]), e4m3x2_f16x2(f.k[1][w] >> 16));
+        }
+        const float f0 = kscale * qs[0], f1 = kscale * qs[1];
+        float x[8] = {s0[0] * f0, s0[1] * f0, s1[0] * f0, s1[1] * f0, s0[2] * f1, s0[3] * f1, s1[2] * f1, s1[3] * f1};
+        bool nans = false;
+        if (key + kAttnStep > every) {  // some row does not see some key of this step
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t kk = key + 2 * t + (i & 1) + 8 * (i >> 1);
+                if (kk >= lim0) x[i] = -INFINITY;
+                if (kk >= lim1) x[4 + i] = -INFINITY;
+                uint32_t any = 0;
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    if (kk >= most) f.v[i][w] = 0;  // beyond the last row's keys: whatever lies there
+                    any |= nan_bytes(f.v[i][w]);
+                }
+                nans = nans || any != 0;
+            }
+            nans = __any_sync(0xffffffffu, nans);
+        }
+        // log2 of the V scale; scales below 2^-100 (and 0) weigh as 2^-100 in the maximum only
+        const float lv = log2f(fmaxf(vscale, 0x1p-100f));
+        float t0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), t1 = fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]));
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2)) + lv;
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2)) + lv;
+        if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {
+            const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+            const float a0 = n0 == -INFINITY ? 1.0f : exp2_approx(m0 - n0), a1 = n1 == -INFINITY ? 1.0f : exp2_approx(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                o[j][0] *= a0;
+                o[j][1] *= a0;
+                o[j][2] *= a1;
+                o[j][3] *= a1;
+            }
+        }
+        const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = exp2_approx(x[i] - b0);
+            x[4 + i] = exp2_approx(x[4 + i] - b1);
+            l0 += x[i];
+            l1 += x[4 + i];
+        }
+        const float wv = vscale * 0x1p14f;
+        const uint32_t p0 = f16x2_pack(x[0] * wv, x[1] * wv), p1 = f16x2_pack(x[4] * wv, x[5] * wv),
+                       p2 = f16x2_pack(x[2] * wv, x[3] * wv), p3 = f16x2_pack(x[6] * wv, x[7] * wv);
+        if (nans) {
+            // A NaN code of V reaches the rows that see its key and no other: it is
+            // taken out of the product, and the rows that see one are counted.
+            uint32_t see[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // a0: row g, a1: row g + 8 of keys 2t, 2t + 1; a2, a3: of keys 8 + 2t, ...
+                const int64_t kk = key + 2 * t + 8 * (i >> 1);
+                const int lim = (i & 1) ? lim1 : lim0;
+                see[i] = (kk < lim ? 0x3c00u : 0u) | (kk + 1 < lim ? 0x3c000000u : 0u);
+            }
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t one[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t lo = (nan_bytes(f.v[2 * h][w]) >> (8 * e)) & 1u, hi = (nan_bytes(f.v[2 * h + 1][w]) >> (8 * e)) & 1u;
+                        one[h] = (lo ? 0x3c00u : 0u) | (hi ? 0x3c000000u : 0u);
+                    }
+                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma_f16(c, see[0], see[1], see[2], see[3], one[0], one[1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c[i] > 0.0f) o[4 * w + e][i] = __int_as_float(0x7fffffff);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f.v[i][w] &= ~nan_bytes(f.v[i][w]);
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+            const uint32_t lo0 = __byte_perm(f.v[0][w], f.v[1][w], 0x5140), hi0 = __byte_perm(f.v[0][w], f.v[1][w], 0x7362);
+            const uint32_t lo1 = __byte_perm(f.v[2][w], f.v[3][w], 0x5140), hi1 = __byte_perm(f.v[2][w], f.v[3][w], 0x7362);
+            mma_f16(o[4 * w], p0, p1, p2, p3, e4m3x2_f16x2(lo0), e4m3x2_f16x2(lo1));
+            mma_f16(o[4 * w + 1], p0, p1, p2, p3, e4m3x2_f16x2(lo0 >> 16), e4m3x2_f16x2(lo1 >> 16));
+            mma_f16(o[4 * w + 2], p0, p1, p2, p3, e4m3x2_f16x2(hi0), e4m3x2_f16x2(hi1));
+            mma_f16(o[4 * w + 3], p0, p1, p2, p3, e4m3x2_f16x2(hi0 >> 16), e4m3x2_f16x2(hi1 >> 16));
+        }
+    }
+
+    // join the four warps: sums under the common maximum
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (t == 0) {
+        red_m[warp][g] = m0;
+        red_m[warp][g + 8] = m1;
+        red_l[warp][g] = l0;
+        red_l[warp][g + 8] = l1;
+    }
+    __syncthreads();  // also: every warp is done with the page ids
+    float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        top0 = fmaxf(top0, red_m[w][g]);
+        top1 = fmaxf(top1, red_m[w][g + 8]);
+    }
+    const float a0 = m0 == -INFINITY ? 0.0f : exp2_approx(m0 - top0), a1 = m1 == -INFINITY ? 0.0f : exp2_approx(m1 - top1);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {  // columns 2t, 2t + 1 of tile j: dims D/8 (2t) + j, D/8 (2t + 1) + j
+        float* row0 = red + (warp * kAttnRows + g) * (D + 4);
+        float* row1 = row0 + 8 * (D + 4);
+        row0[2 * t * NJ + j] = o[j][0] * a0;
+        row0[(2 * t + 1) * NJ + j] = o[j][1] * a0;
+        row1[2 * t * NJ + j] = o[j][2] * a1;
+        row1[(2 * t + 1) * NJ + j] = o[j][3] * a1;
+    }
+    __syncthreads();
+    // a warp finishes four rows, a lane D / 32 dims of each
+    for (int r = warp; r < rows; r += kWarps) {
+        float top = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red_m[w][r]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) l += red_m[w][r] == -INFINITY ? red_l[w][r] : red_l[w][r] * exp2_approx(red_m[w][r] - top);
+        float v[D / 32];
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+            v[d] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v[d] += red[(w * kAttnRows + r) * (D + 4) + lane * (D / 32) + d];
+        }
+        const int64_t row = r0 + r;
+        if (sp.ws) {
+            float* slot = sp.ws + ((((b * p.c.heads + hk) * sp.row_tiles + rt) * sp.slot_rows + r) * sp.splits + split) * kAttnSlot<D>;
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) slot[lane * (D / 32) + d] = v[d];
+            if (lane == 0) {
+                slot[D] = top;
+                slot[D + 1] = l;
+            }
+        } else {
+            const int64_t tok = s.first + row / p.group, h = (int64_t)hk * p.group + row % p.group;
+            const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + lane * (D / 32));
+#pragma unroll
+            for (int d = 0; d < D / 32; d += 2) dst[d / 2] = bf16x2_pack(v[d] * inv, v[d + 1] * inv);
+            if (p.lse && lane == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+        }
+    }
+}
+
+// Joins the splits of a row: one warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, const AttnSplit sp) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
-    int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int h = (int)(i % p.q_heads);
-    i /= p.q_heads;
-    const int64_t row = i % p.max_q, b = i / p.max_q;
+    int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const float* slots = sp.ws + u * sp.splits * kAttnSlot<D>;
+    const int64_t in_tile = u % sp.slot_rows;
+    u /= sp.slot_rows;
+    const int64_t row = u % sp.row_tiles * kAttnRows + in_tile;
+    u /= sp.row_tiles;
+    const int hk = (int)(u % p.c.heads);
+    const int64_t b = u / p.c.heads;
     if (b >= p.batch) return;
-    const AttnSeq s = attn_seq(p, b, lane == 0);
-    if (row >= s.n) return;
-    const int hk = h / p.group;
-    const uint16_t* q = p.q + (s.first + row) * p.ldq + (int64_t)h * D + lane * N;
-    float qv[N], o[N];
+    const AttnSeq s = attn_seq(p, b, false);
+    if (row >= s.n * p.group) return;
+    // the splits that its row tile filled (the first always)
+    const int64_t last = min64(s.n * p.group, (row / kAttnRows + 1) * kAttnRows) - 1;
+    const int64_t most = attn_limit(p, s, last);
+    const int n = most > sp.chunk ? (int)((most + sp.chunk - 1) / sp.chunk) : 1;
+    float top = -INFINITY;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, slots[i * kAttnSlot<D> + D]);
 #pragma unroll
-    for (int t = 0; t < N; ++t) {
-        qv[t] = __uint_as_float((uint32_t)q[t] << 16) * p.scale_log2;
-        o[t] = 0.0f;
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    float l = 0.0f, v[D / 32];
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) v[d] = 0.0f;
+    for (int i = 0; i < n; ++i) {
+        const float* slot = slots + i * kAttnSlot<D>;
+        const float m = slot[D], a = m == -INFINITY ? 1.0f : exp2_approx(m - top);
+        l = fmaf(slot[D + 1], a, l);
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) v[d] = fmaf(slot[lane * (D / 32) + d], a, v[d]);
     }
-    const int64_t keys = p.causal ? s.len - s.n + row + 1 : s.len;
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t j = 0; j < keys; ++j) {
-        const int64_t at = attn_page(p, b, j / p.c.page, lane == 0) * p.c.heads + hk;
-        const int64_t off = (at * p.c.page + j % p.c.page) * D + lane * N;
-        float dot = 0.0f;
+    const int64_t tok = s.first + row / p.group, h = (int64_t)hk * p.group + row % p.group;
+    const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + lane * (D / 32));
 #pragma unroll
-        for (int t = 0; t < N; ++t) dot = fmaf(qv[t], e4m3_decode(p.c.k[off + t]), dot);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
-        dot *= p.c.k_scale[at];
-        const float top = fmaxf(m, dot), keep = exp2f(m - top), w = exp2f(dot - top);
-        const float vs = p.c.v_scale[at];
-        l = l * keep + w;
-#pragma unroll
-        for (int t = 0; t < N; ++t) o[t] = fmaf(o[t], keep, w * vs * e4m3_decode(p.c.v[off + t]));
-        m = top;
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int t = 0; t < N; ++t)
-        p.o[(s.first + row) * p.ldo + (int64_t)h * D + lane * N + t] = (uint16_t)bf16x2_pack(o[t] * inv, 0.0f);
-    if (p.lse && lane == 0) p.lse[(s.first + row) * p.q_heads + h] = keys > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+    for (int d = 0; d < D / 32; d += 2) dst[d / 2] = bf16x2_pack(v[d] * inv, v[d + 1] * inv);
+    if (p.lse && lane == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
 }  // namespace fp4q

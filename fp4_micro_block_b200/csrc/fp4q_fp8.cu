@@ -274,12 +274,57 @@ FP4Q_API fp4q_status fp4q_kv_append_fp8(const void* k, int64_t ldk, const void* 
                   (cudaStream_t)stream, p);
 }
 
+namespace {
+
+// How the rows and keys of a call are cut.  The keys of a row tile are split
+// where there are too few tiles to fill the GPU (by the lengths' bound, since
+// the lengths are on the device).
+struct AttnPlan {
+    int64_t row_tiles, splits, chunk, slot_rows;
+    size_t ws_bytes;
+};
+
+fp4q_status attn_plan(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_heads, int64_t kv_heads, int64_t dim,
+                      int sms, AttnPlan* out) {
+    AttnPlan a{};
+    if (max_q >= kMaxDim / (q_heads / kv_heads)) return FP4Q_ERR_UNSUPPORTED;
+    a.row_tiles = spans(max_q * (q_heads / kv_heads), kAttnRows);
+    if (a.row_tiles >= kMaxDim / kv_heads || a.row_tiles * kv_heads >= kMaxDim / batch) return FP4Q_ERR_UNSUPPORTED;
+    a.slot_rows = std::min<int64_t>(kAttnRows, max_q * (q_heads / kv_heads));
+    const int64_t items = batch * kv_heads * a.row_tiles;
+    const int64_t want = std::max<int64_t>(1, spans(6 * (int64_t)sms, items));
+    a.chunk = std::min<int64_t>(kAttnMaxChunk, std::max<int64_t>(128, spans(spans(max_len, want), 128) * 128));
+    a.splits = std::max<int64_t>(1, spans(max_len, a.chunk));
+    if (a.splits >= kMaxDim / items || items >= kMaxDim / kAttnRows) return FP4Q_ERR_UNSUPPORTED;
+    a.ws_bytes = a.splits > 1 ? (size_t)(items * a.splits * a.slot_rows * (dim + 2)) * sizeof(float) : 0;
+    *out = a;
+    return FP4Q_OK;
+}
+
+template <int D>
+fp4q_status launch_attn(const AttnParams& p, const AttnPlan& a, void* ws, cudaStream_t s) {
+    AttnSplit sp{a.row_tiles, a.splits, a.chunk, (int32_t)a.slot_rows, a.splits > 1 ? static_cast<float*>(ws) : nullptr};
+    const int64_t items = p.batch * p.c.heads * a.row_tiles;
+    fp4q_status st = launch(attn_rows_kernel<D>, (int)(items * a.splits), 32 * kAttnWarps<D>, 0, s, p, sp);
+    if (st != FP4Q_OK || a.splits == 1) return st;
+    return launch(attn_join_kernel<D>, (int)spans(items * a.slot_rows, 4), 128, 0, s, p, sp);
+}
+
+}  // namespace
+
 FP4Q_API size_t fp4q_attention_fp8_workspace_bytes(int64_t batch, int64_t max_q, int64_t max_len, int32_t num_q_heads,
                                                    int32_t num_kv_heads, int32_t head_dim) {
+    const size_t bad = (size_t)-1;
     if (batch < 0 || max_q < 0 || max_len < 0 || num_kv_heads <= 0 || num_q_heads <= 0 ||
-        num_q_heads % num_kv_heads != 0 || head_dim <= 0)
-        return (size_t)-1;
-    return 0;
+        num_q_heads % num_kv_heads != 0 || head_dim <= 0 || batch >= kMaxDim || max_q >= kMaxDim || max_len >= kMaxDim)
+        return bad;
+    if (batch == 0 || max_q == 0) return 0;
+    int sms = 0;
+    AttnPlan a;
+    if (sm_count(&sms) != FP4Q_OK ||
+        attn_plan(batch, max_q, max_len, num_q_heads, num_kv_heads, head_dim, sms, &a) != FP4Q_OK)
+        return bad;
+    return a.ws_bytes;
 }
 
 FP4Q_API fp4q_status fp4q_attention_fp8(const void* q, int64_t ldq, int64_t tokens, int32_t num_q_heads,
@@ -319,10 +364,15 @@ FP4Q_API fp4q_status fp4q_attention_fp8(const void* q, int64_t ldq, int64_t toke
     p.o = static_cast<uint16_t*>(o);
     p.ldo = ldo;
     p.lse = lse;
-    const int64_t warps = max_q * batch;
-    if (warps >= kMaxDim / num_q_heads) return FP4Q_ERR_UNSUPPORTED;
-    const int grid = (int)spans(warps * num_q_heads, 4);
-    if (p.c.dim == 64) return launch(attn_simple_kernel<64>, grid, 128, 0, (cudaStream_t)stream, p);
-    if (p.c.dim == 128) return launch(attn_simple_kernel<128>, grid, 128, 0, (cudaStream_t)stream, p);
-    return launch(attn_simple_kernel<256>, grid, 128, 0, (cudaStream_t)stream, p);
+    int sms = 0;
+    AttnPlan a;
+    if ((st = sm_count(&sms)) != FP4Q_OK) return st;
+    if ((st = attn_plan(batch, max_q, max_len, num_q_heads, p.c.heads, p.c.dim, sms, &a)) != FP4Q_OK) return st;
+    if (a.ws_bytes > 0) {
+        if (!workspace || workspace_bytes < a.ws_bytes) return FP4Q_ERR_INVALID_ARG;
+        if (!aligned(workspace, 16)) return FP4Q_ERR_ALIGNMENT;
+    }
+    if (p.c.dim == 64) return launch_attn<64>(p, a, workspace, (cudaStream_t)stream);
+    if (p.c.dim == 128) return launch_attn<128>(p, a, workspace, (cudaStream_t)stream);
+    return launch_attn<256>(p, a, workspace, (cudaStream_t)stream);
 }
