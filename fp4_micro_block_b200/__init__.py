@@ -14,9 +14,8 @@ with torch and call the entry points.
 from __future__ import annotations
 
 import ctypes as C
-import functools
-import math
 import os
+import struct
 
 import torch
 
@@ -102,7 +101,9 @@ class _Lazy:
     def __getattr__(self, name):
         if _Lazy._cdll is None:
             _Lazy._cdll = _load()
-        return getattr(_Lazy._cdll, name)
+        fn = getattr(_Lazy._cdll, name)
+        self.__dict__[name] = fn  # later uses find it without this call
+        return fn
 
 
 _lib = _Lazy()
@@ -257,42 +258,58 @@ def fp4q_selftest_div(x, d, q_fast, q_ieee, stream=None):
 
 # ----------------------------------------------------------------------------- 8-bit entry points
 
-def _on_device(fn):
-    """Runs the call with the first tensor's device current (the library launches on the
-    current device, and the default stream is that device's current one); the other tensors
-    have to be there too."""
-    @functools.wraps(fn)
-    def call(*args, **kwargs):
-        tensors = [a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)]
-        for t in tensors:
-            if not t.is_cuda:
-                raise ValueError("fp4q entry points take CUDA tensors")
-            if t.device != tensors[0].device:
-                raise ValueError(f"{fn.__name__}: tensors on {tensors[0].device} and {t.device}")
-        if not tensors or tensors[0].device.index == torch.cuda.current_device():
-            return fn(*args, **kwargs)
-        with torch.cuda.device(tensors[0].device):
-            return fn(*args, **kwargs)
-    return call
+# A call costs the host about as much as its kernel costs the GPU, so these keep
+# to cheap tensor queries.
+
+def _device(where, *tensors):
+    """The CUDA device index that all of them (but None) are on."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: tensors on {tensors[0].device} and {t.device}")
+    if dev < 0:
+        raise ValueError("fp4q entry points take CUDA tensors")
+    return dev
+
+
+def _launch(where, dev, fn, args, stream):
+    """fn(*args, stream) with device `dev` current (the library launches on the current
+    device, and the default stream is that device's current one)."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != FP4Q_OK:
+        raise Fp4qError(status, where)
+    return status
 
 
 def _want(t, name, dtypes, *shape):
     """A tensor argument's type and shape (None: any size) against what the call takes."""
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d).replace('torch.', '') for d in dtypes)}, not {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, not {tuple(t.shape)}")
+    got = t.shape
+    if got != shape and (len(got) != len(shape) or any(w is not None and w != n for w, n in zip(shape, got))):
+        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, not {tuple(got)}")
 
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+_KV = struct.Struct("<5q3i4x2q")  # fp4q_kv_cache
 
 
-def _row_stride(t, name):
-    """Row stride of a 2-D row-major view."""
-    if t.shape[1] > 1 and t.stride(1) != 1:
+def _row_stride(t, name, unit):
+    """Row stride of a 2-D row-major view; for a single row, whose stride says nothing, the next multiple of `unit`."""
+    ld, step = t.stride()
+    rows, cols = t.shape
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must be a row-major view (unit column stride)")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return ld if rows > 1 else -(-cols // unit) * unit
 
 
 def _fp8_rows(n, block):
@@ -301,62 +318,63 @@ def _fp8_rows(n, block):
 
 def _fp8_side(codes, scales, rows, cols, block, what):
     """Codes [rows, cols] and scales [ceil(cols/128), rows or tile rows]: their strides."""
-    _want(codes, f"{what} codes", _CODES, rows, cols)
-    _want(scales, f"{what} scales", _F32, -(-cols // 128), _fp8_rows(rows, block))
-    return _lead(codes, f"{what} codes", 16), _lead(scales, f"{what} scales", 4)
+    _want(codes, what, _CODES, rows, cols)
+    _want(scales, what, _F32, -(-cols // 128), _fp8_rows(rows, block))
+    return _row_stride(codes, what, 16), _row_stride(scales, what, 4)
 
 
-def _lead(t, name, unit):
-    """The row stride; for a single row, whose stride says nothing, the next multiple of `unit`."""
-    return _row_stride(t, name) if t.shape[0] > 1 else -(-t.shape[1] // unit) * unit
-
-
-@_on_device
 def fp4q_quantize_fp8(x, block, codes=None, scales=None, codes_t=None, scales_t=None, stream=None):
     """E4M3 codes and block-128 scales of bf16 x [M, K] and / or of its transpose."""
     _want(x, "x", _BF16, None, None)
     M, K = x.shape
-    ldc, lds = _fp8_side(codes, scales, M, K, block, "x") if codes is not None else (0, 0)
-    ldct, ldst = _fp8_side(codes_t, scales_t, K, M, block, "transposed") if codes_t is not None else (0, 0)
-    return _check(_lib.fp4q_quantize_fp8(_ptr(x), M, K, _lead(x, "x", 8), int(block), _ptr(codes), ldc, _ptr(scales),
-                                         lds, _ptr(codes_t), ldct, _ptr(scales_t), ldst, _stream(stream)),
-                  "fp4q_quantize_fp8")
+    dev = _device("fp4q_quantize_fp8", x, codes, scales, codes_t, scales_t)
+    c = s = ct = st = None
+    ldc = lds = ldct = ldst = 0
+    if codes is not None:
+        ldc, lds = _fp8_side(codes, scales, M, K, block, "codes / scales")
+        c, s = codes.data_ptr(), scales.data_ptr()
+    if codes_t is not None:
+        ldct, ldst = _fp8_side(codes_t, scales_t, K, M, block, "codes_t / scales_t")
+        ct, st = codes_t.data_ptr(), scales_t.data_ptr()
+    return _launch("fp4q_quantize_fp8", dev, _lib.fp4q_quantize_fp8,
+                   (x.data_ptr(), M, K, _row_stride(x, "x", 8), block, c, ldc, s, lds, ct, ldct, st, ldst), stream)
 
 
-@_on_device
 def fp4q_gemm_fp8(a_codes, a_scales, b_codes, b_scales, b_block, d, stream=None):
     """d [M, N] (float32 or bfloat16) = A B^T of two fp4q_quantize_fp8 outputs (A: row blocks)."""
     _want(d, "d", (torch.float32, torch.bfloat16), None, None)
     M, N = d.shape
     K = a_codes.shape[-1]
-    lda, ldas = _fp8_side(a_codes, a_scales, M, K, FP4Q_FP8_ROW, "A")
-    ldb, ldbs = _fp8_side(b_codes, b_scales, N, K, b_block, "B")
-    return _check(_lib.fp4q_gemm_fp8(_ptr(a_codes), lda, _ptr(a_scales), ldas, _ptr(b_codes), ldb, _ptr(b_scales), ldbs,
-                                     int(b_block), M, N, K, _ptr(d), _row_stride(d, "d"),
-                                     int(d.dtype == torch.bfloat16), _stream(stream)), "fp4q_gemm_fp8")
+    dev = _device("fp4q_gemm_fp8", d, a_codes, a_scales, b_codes, b_scales)
+    lda, ldas = _fp8_side(a_codes, a_scales, M, K, FP4Q_FP8_ROW, "A's codes / scales")
+    ldb, ldbs = _fp8_side(b_codes, b_scales, N, K, b_block, "B's codes / scales")
+    return _launch("fp4q_gemm_fp8", dev, _lib.fp4q_gemm_fp8,
+                   (a_codes.data_ptr(), lda, a_scales.data_ptr(), ldas, b_codes.data_ptr(), ldb, b_scales.data_ptr(), ldbs,
+                    b_block, M, N, K, d.data_ptr(), _row_stride(d, "d", 1), d.dtype is torch.bfloat16), stream)
 
 
 def _token_stride(t, name):
     """Stride between tokens of [tokens, heads, dim] whose heads and dims are contiguous."""
     T, H, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"{name}: heads and dims of a token must be contiguous")
-    return t.stride(0) if T > 1 else H * D
+    return st if T > 1 else H * D
 
 
 def _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table):
+    """The bytes of an fp4q_kv_cache, its head count and head dim."""
     _want(k_cache, "k_cache", _CODES, None, None, None, None)
     pages, heads, page, dim = k_cache.shape
     _want(v_cache, "v_cache", _CODES, pages, heads, page, dim)
     _want(k_scale, "k_scale", _F32, pages, heads)
     _want(v_scale, "v_scale", _F32, pages, heads)
     _want(block_table, "block_table", _I32, None, None)
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"),
-                 (block_table, "block_table")):
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
-    return Fp4qKvCache(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), pages, heads, page, dim,
-                       _ptr(block_table), block_table.shape[1])
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and
+            v_scale.is_contiguous() and block_table.is_contiguous()):
+        raise ValueError("the cache, its scales and the block table must be contiguous")
+    return _KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads, page,
+                    dim, block_table.data_ptr(), block_table.shape[1]), heads, dim
 
 
 def _ragged(cu, lens, block_table, name):
@@ -368,16 +386,17 @@ def _ragged(cu, lens, block_table, name):
     return B
 
 
-@_on_device
 def fp4q_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, lens, max_new, stream=None):
     """Writes the new tokens k, v [tokens, Hkv, D] (bf16) at the end of their sequences."""
-    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table)
-    _want(k, "k", _BF16, None, cache.num_kv_heads, cache.head_dim)
-    _want(v, "v", _BF16, *k.shape)
+    dev = _device("fp4q_kv_append_fp8", k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, lens)
+    cache, heads, dim = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+    T = k.shape[0]
+    _want(k, "k", _BF16, T, heads, dim)
+    _want(v, "v", _BF16, T, heads, dim)
     B = _ragged(cu_new, lens, block_table, "cu_new")
-    return _check(_lib.fp4q_kv_append_fp8(_ptr(k), _token_stride(k, "k"), _ptr(v), _token_stride(v, "v"), k.shape[0],
-                                          C.addressof(cache), _ptr(cu_new), _ptr(lens), B, int(max_new),
-                                          _stream(stream)), "fp4q_kv_append_fp8")
+    return _launch("fp4q_kv_append_fp8", dev, _lib.fp4q_kv_append_fp8,
+                   (k.data_ptr(), _token_stride(k, "k"), v.data_ptr(), _token_stride(v, "v"), T, cache,
+                    cu_new.data_ptr(), lens.data_ptr(), B, max_new), stream)
 
 
 def fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, num_q_heads, num_kv_heads, head_dim):
@@ -387,25 +406,25 @@ def fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, num_q_heads, num_k
     return n
 
 
-@_on_device
 def fp4q_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, max_q, max_len, o, lse=None,
                        causal=True, softmax_scale=None, workspace=None, stream=None):
     """o [tokens, Hq, D] (bf16) = attention of q [tokens, Hq, D] (bf16) over the cache."""
-    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table)
-    _want(q, "q", _BF16, None, None, cache.head_dim)
-    _want(o, "o", _BF16, *q.shape)
+    dev = _device("fp4q_attention_fp8", q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, o, lse, workspace)
+    cache, _, dim = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table)
     T, Hq, D = q.shape
+    _want(q, "q", _BF16, T, Hq, dim)
+    _want(o, "o", _BF16, T, Hq, dim)
     B = _ragged(cu_q, lens, block_table, "cu_q")
     if lse is not None:
         _want(lse, "lse", _F32, T, Hq)
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
-    scale = 1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    return _check(_lib.fp4q_attention_fp8(_ptr(q), _token_stride(q, "q"), T, Hq, C.addressof(cache), _ptr(cu_q),
-                                          _ptr(lens), B, int(max_q), int(max_len), int(bool(causal)), scale, _ptr(o),
-                                          _token_stride(o, "o"), _ptr(lse), _ptr(workspace), ws_bytes,
-                                          _stream(stream)), "fp4q_attention_fp8")
+    scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return _launch("fp4q_attention_fp8", dev, _lib.fp4q_attention_fp8,
+                   (q.data_ptr(), _token_stride(q, "q"), T, Hq, cache, cu_q.data_ptr(), lens.data_ptr(), B, max_q,
+                    max_len, bool(causal), scale, o.data_ptr(), _token_stride(o, "o"),
+                    None if lse is None else lse.data_ptr(), ws, ws_bytes), stream)
 
 
 # ----------------------------------------------------------------------------- allocating helpers
@@ -512,8 +531,8 @@ def alloc_fp8(rows, cols, block=FP4Q_FP8_ROW, device="cuda"):
     """codes [rows, cols] u8 and scales [ceil(cols/128), rows or ceil(rows/128)] f32, as views of
     buffers whose rows are 16-byte aligned."""
     n = _fp8_rows(rows, block)
-    codes = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=device)[:, :cols]
-    scales = torch.empty((-(-cols // 128), -(-n // 4) * 4), dtype=torch.float32, device=device)[:, :n]
+    codes = torch.empty_strided((rows, cols), (-(-cols // 16) * 16, 1), dtype=torch.uint8, device=device)
+    scales = torch.empty_strided((-(-cols // 128), n), (-(-n // 4) * 4, 1), dtype=torch.float32, device=device)
     return codes, scales
 
 
