@@ -58,10 +58,11 @@ __device__ __forceinline__ int64_t attn_page(const AttnParams& p, int64_t b, int
 //
 // One CTA: one sequence, one K/V head, 16 rows (query i, head g of the group:
 // row i * G + g) and one run of keys; four warps take turns of 16 keys, which
-// lie within one page.  Decoding is bound by reading the cache, so the codes go
-// from global memory straight into the registers that the tensor cores read,
-// each lane loading whole 16-byte pieces: which of a product's k (or n) indices
-// a lane's bytes stand for is free as long as both operands agree.
+// lie within one page.  Decoding is bound by reading the cache: each warp keeps a
+// ring of such steps on its way (TMA boxes of 16 rows, swizzled so that the reads
+// below have no bank conflicts), and lanes read whole 16-byte pieces of codes:
+// which of a product's k (or n) indices a lane's bytes stand for is free as long
+// as both operands agree.
 //   S = Q K^T: lane (g, t) = (lane / 4, lane % 4) holds dims D/4 t .. of key g
 //     (and 8 + g); its next four bytes are the k indices 2t, 2t+1, 2t+8, 2t+9
 //     of the next m16n8k16 step.
@@ -89,19 +90,6 @@ __device__ __forceinline__ uint32_t f16x2_pack(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// 16 bytes that are read once.
-__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint2 ld_stream8(const uint8_t* p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
-}
 __device__ __forceinline__ float exp2_approx(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -114,7 +102,7 @@ template <int D>
 constexpr int kAttnSlot = D + 2;
 
 constexpr int kAttnRows = 16, kAttnStep = 16;
-constexpr int kAttnMaxChunk = 16384;  // keys of one split: its pages' ids and scales are in shared memory
+constexpr int kAttnMaxChunk = 4096;   // keys of one split: its pages' ids and scales are in shared memory
 
 struct AttnSplit {
     int64_t row_tiles, splits;
@@ -130,61 +118,74 @@ __device__ __forceinline__ int attn_limit(const AttnParams& p, const AttnSeq& s,
     return i < s.n && lim > 0 ? (int)lim : 0;
 }
 
+// A step's codes of K or V in shared memory: boxes of 16 rows x min(D, 128)
+// bytes, whose 16-byte pieces the TMA's swizzle permutes within a row.
 template <int D>
-constexpr int kAttnWarps = D == 256 ? 2 : 4;  // (the sums of four would not fit in 48 KiB)
-
-template <int D>
-struct AttnFrag {
-    static constexpr int kw = D / 16;  // words of a lane's part of one key of K: D/4 bytes
-    static constexpr int vw = D / 32;  // words of a lane's part of one key of V: D/8 bytes
-    uint32_t k[2][kw], v[4][vw];
+struct AttnTile {
+    static constexpr int box_cols = D < 128 ? D : 128;
+    static constexpr int bytes = kAttnStep * D;
+    // Offset of byte c (a multiple of 8) of row r.
+    __device__ static __forceinline__ uint32_t at(int r, int c) {
+        if constexpr (D == 64)
+            return r * 64 + ((((c >> 4) ^ (r >> 1)) & 3) << 4) + (c & 15);
+        else
+            return (c >> 7) * (kAttnStep * 128) + r * 128 + ((((c >> 4) ^ r) & 7) << 4) + (c & 15);
+    }
 };
 
-template <int D>
-__device__ __forceinline__ void attn_load(AttnFrag<D>& f, const uint8_t* kp, const uint8_t* vp, int g, int t) {
-    // kp, vp: the step's first key of this head's page
+// N words of row r from byte c.
+template <int D, int N>
+__device__ __forceinline__ void ld_words(uint32_t (&w)[N], const uint8_t* tile, int r, int c) {
+    if constexpr (N == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(tile + AttnTile<D>::at(r, c));
+        w[0] = x.x;
+        w[1] = x.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint8_t* src = kp + (g + 8 * i) * D + t * (D / 4);
-#pragma unroll
-        for (int w = 0; w < D / 16; w += 4) {
-            const uint4 x = ld_stream(src + 4 * w);
-            f.k[i][w] = x.x;
-            f.k[i][w + 1] = x.y;
-            f.k[i][w + 2] = x.z;
-            f.k[i][w + 3] = x.w;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint8_t* src = vp + (2 * t + (i & 1) + 8 * (i >> 1)) * D + g * (D / 8);
-        if constexpr (D == 64) {
-            const uint2 x = ld_stream8(src);
-            f.v[i][0] = x.x;
-            f.v[i][1] = x.y;
-        } else {
-#pragma unroll
-            for (int w = 0; w < D / 32; w += 4) {
-                const uint4 x = ld_stream(src + 4 * w);
-                f.v[i][w] = x.x;
-                f.v[i][w + 1] = x.y;
-                f.v[i][w + 2] = x.z;
-                f.v[i][w + 3] = x.w;
-            }
+        for (int i = 0; i < N; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(tile + AttnTile<D>::at(r, c + 4 * i));
+            w[i] = x.x;
+            w[i + 1] = x.y;
+            w[i + 2] = x.z;
+            w[i + 3] = x.w;
         }
     }
 }
+
+// Shared memory of attn_rows_kernel.
+template <int D>
+struct AttnGeo {
+    static constexpr int warps = 4;
+    static constexpr int stages = D == 256 ? 3 : 4;
+    static constexpr int ctas = D == 256 ? 1 : D == 128 ? 3 : 4;  // per SM, for the register budget
+    static constexpr int stage_bytes = 2 * AttnTile<D>::bytes;
+    static constexpr int ring = warps * stages * stage_bytes;
+    static constexpr int pages = kAttnMaxChunk / 16;
+    static constexpr int red = warps * kAttnRows * (D + 4) * 4;  // the warps' sums, in the ring's place
+    static constexpr int qf_off = ring > red ? ring : red;
+    static constexpr int ids_off = qf_off + D / 16 * 32 * 16;
+    static constexpr int ml_off = ids_off + 3 * 4 * pages;
+    static constexpr int bar_off = ml_off + 2 * 4 * warps * kAttnRows;
+    static constexpr int smem = 1024 + bar_off + 8 * warps * stages;
+};
 
 // Bytes of w that are NaN codes, as 0xff; the others 0.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
 template <int D>
-__global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const AttnParams p, const AttnSplit sp) {
-    constexpr int KW = D / 16, NJ = D / 8, kWarps = kAttnWarps<D>;
-    // row sums of the four warps; pages' ids and scales before
-    __shared__ __align__(16) float red[kWarps * kAttnRows * (D + 4)];
-    __shared__ float red_m[kWarps][kAttnRows], red_l[kWarps][kAttnRows];
-    static_assert(sizeof(red) >= 3 * 4 * kAttnMaxChunk / 16, "page ids and scales fit");
+__global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
+    attn_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const AttnParams p, const AttnSplit sp) {
+    using G = AttnGeo<D>;
+    constexpr int KW = D / 16, NJ = D / 8, kWarps = G::warps, S = G::stages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = align_shared<1024>(smem_raw);
+    float* red = reinterpret_cast<float*>(smem);
+    uint4(*qf)[32] = reinterpret_cast<uint4(*)[32]>(smem + G::qf_off);  // the queries as fragments, for every warp
+    int32_t* ids = reinterpret_cast<int32_t*>(smem + G::ids_off);       // the split's pages: row / page, scales
+    float *ks = reinterpret_cast<float*>(ids + G::pages), *vs = ks + G::pages;
+    float(*red_m)[kAttnRows] = reinterpret_cast<float(*)[kAttnRows]>(smem + G::ml_off);
+    float(*red_l)[kAttnRows] = red_m + kWarps;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -208,8 +209,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const Att
 
     // page ids and scales of the split
     const int n_pages = k0 < k1 ? (int)((k1 - k0 + p.c.page - 1) / p.c.page) : 0;
-    int32_t* ids = reinterpret_cast<int32_t*>(red);
-    float *ks = red + kAttnMaxChunk / 16, *vs = ks + kAttnMaxChunk / 16;
     for (int i = threadIdx.x; i < n_pages; i += 32 * kWarps) {
         const int64_t at = attn_page(p, b, k0 / p.c.page + i, true) * p.c.heads + hk;
         ids[i] = (int32_t)at;
@@ -218,24 +217,18 @@ __global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const Att
     }
 
     // this lane's part of the queries: rows g and g + 8, dims D/4 t .. D/4 t + D/4 - 1, scaled by a power of two
-    uint32_t qa[KW][4];
     float qs[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int64_t r = r0 + g + 8 * i;
         const bool live = r < s.n * p.group;
         const uint16_t* src = p.q + (s.first + (live ? r / p.group : 0)) * p.ldq + ((int64_t)hk * p.group + (live ? r % p.group : 0)) * D + t * (D / 4);
-        uint32_t w[D / 8];
+        uint4 x[D / 32];
         float amax = 0.0f;
 #pragma unroll
-        for (int c = 0; c < D / 8; c += 4) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (live) x = __ldg(reinterpret_cast<const uint4*>(src + 2 * c));
-            w[c] = x.x;
-            w[c + 1] = x.y;
-            w[c + 2] = x.z;
-            w[c + 3] = x.w;
-            amax = fmaxf(amax, amax8(x));
+        for (int c = 0; c < D / 32; ++c) {
+            x[c] = live ? __ldg(reinterpret_cast<const uint4*>(src + 8 * c)) : make_uint4(0, 0, 0, 0);
+            amax = fmaxf(amax, amax8(x[c]));
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -245,10 +238,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const Att
         const int e1 = e / 2, e2 = e - e1;
         const float u1 = __int_as_float((127 + e1) << 23), u2 = __int_as_float((127 + e2) << 23);
         qs[i] = __int_as_float((127 - e1) << 23) * __int_as_float((127 - e2) << 23);
+        if (warp == 0) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-            const uint32_t h = f16x2_pack(bf16lo(w[c]) * u1 * u2, bf16hi(w[c]) * u1 * u2);
-            qa[c / 2][i + 2 * (c & 1)] = h;
+            for (int c = 0; c < D / 32; ++c) {
+                const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                for (int h = 0; h < 4; ++h)  // word h of the piece: k step 2c + h/2, its lower or upper two indices
+                    reinterpret_cast<uint32_t*>(&qf[2 * c + h / 2][lane])[i + 2 * (h & 1)] =
+                        f16x2_pack(bf16lo(w[h]) * u1 * u2, bf16hi(w[h]) * u1 * u2);
+            }
         }
     }
     __syncthreads();
@@ -258,19 +256,41 @@ __global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const Att
     for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
 
-    const int64_t plane = (int64_t)p.c.page * D;
     const int steps = k0 < k1 ? (int)((k1 - k0 + kAttnStep - 1) / kAttnStep) : 0;
     const int per_page = p.c.page / kAttnStep, shift = per_page == 1 ? 0 : per_page == 2 ? 1 : per_page == 4 ? 2 : 3;
-    auto load = [&](AttnFrag<D>& f, int st) {
-        const int64_t at = ids[st >> shift] * plane + (int64_t)(st & (per_page - 1)) * kAttnStep * D;
-        attn_load<D>(f, p.c.k + at, p.c.v + at, g, t);
+    uint8_t* ring = smem + warp * (S * G::stage_bytes);
+    const uint32_t full0 = smem_u32(smem + G::bar_off) + 8 * S * warp;
+    auto fetch = [&](int st, int stage) {  // one lane
+        const uint32_t dst = smem_u32(ring + stage * G::stage_bytes), bar = full0 + 8 * stage;
+        const int32_t row = ids[st >> shift] * p.c.page + (st & (per_page - 1)) * kAttnStep;
+        mbar_arrive_expect_tx(bar, G::stage_bytes);
+#pragma unroll
+        for (int c = 0; c < D; c += AttnTile<D>::box_cols) {
+            tma_load_2d(dst + c * kAttnStep, &map_k, c, row, bar);
+            tma_load_2d(dst + AttnTile<D>::bytes + c * kAttnStep, &map_v, c, row, bar);
+        }
     };
-    AttnFrag<D> cur;
-    if (warp < steps) load(cur, warp);
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(full0 + 8 * i, 1);
+        fence_barrier_init();
+        for (int i = 0; i < S && warp + i * kWarps < steps; ++i) fetch(warp + i * kWarps, i);
+    }
+    __syncwarp();
+    int stage = 0;
+    uint32_t phase = 0;
 #pragma unroll 1
     for (int st = warp; st < steps; st += kWarps) {
-        AttnFrag<D> f = cur;
-        if (st + kWarps < steps) load(cur, st + kWarps);
+        if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * stage, phase))) {
+            if (lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
+            break;
+        }
+        const uint8_t *kt = ring + stage * G::stage_bytes, *vt = kt + AttnTile<D>::bytes;
+        // codes of this lane: keys g, 8 + g of K; 2t, 2t+1, 8+2t, 9+2t of V
+        uint32_t kf[2][D / 16], vf[4][D / 32];
+        ld_words<D>(kf[0], kt, g, t * (D / 4));
+        ld_words<D>(kf[1], kt, g + 8, t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ld_words<D>(vf[i], vt, 2 * t + (i & 1) + 8 * (i >> 1), g * (D / 8));
         const int page = st >> shift;
         const int64_t key = k0 + (int64_t)st * kAttnStep;
         const float kscale = ks[page], vscale = vs[page];
@@ -278,8 +298,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const Att
         float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // keys 2t, 2t+1; 8 + 2t, ...
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-            mma_f16(s0, qa[w][0], qa[w][1], qa[w][2], qa[w][3], e4m3x2_f16x2(f.k[0][w]), e4m3x2_f16x2(f.k[0][w] >> 16));
-            mma_f16(s1, qa[w][0], qa[w][1], qa[w][2], qa[w][3], e4m3x2_f16x2(f.k[1][w]), e4m3x2_f16x2(f.k[1][w] >> 16));
+            const uint4 a = qf[w][lane];
+            mma_f16(s0, a.x, a.y, a.z, a.w, e4m3x2_f16x2(kf[0][w]), e4m3x2_f16x2(kf[0][w] >> 16));
+            mma_f16(s1, a.x, a.y, a.z, a.w, e4m3x2_f16x2(kf[1][w]), e4m3x2_f16x2(kf[1][w] >> 16));
         }
         const float f0 = kscale * qs[0], f1 = kscale * qs[1];
         float x[8] = {s0[0] * f0, s0[1] * f0, s1[0] * f0, s1[1] * f0, s0[2] * f1, s0[3] * f1, s1[2] * f1, s1[3] * f1};
@@ -293,8 +314,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const Att
                 uint32_t any = 0;
 #pragma unroll
                 for (int w = 0; w < D / 32; ++w) {
-                    if (kk >= most) f.v[i][w] = 0;  // beyond the last row's keys: whatever lies there
-                    any |= nan_bytes(f.v[i][w]);
+                    if (kk >= most) vf[i][w] = 0;  // beyond the last row's keys: whatever lies there
+                    any |= nan_bytes(vf[i][w]);
                 }
                 nans = nans || any != 0;
             }
@@ -350,7 +371,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const Att
                     uint32_t one[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t lo = (nan_bytes(f.v[2 * h][w]) >> (8 * e)) & 1u, hi = (nan_bytes(f.v[2 * h + 1][w]) >> (8 * e)) & 1u;
+                        const uint32_t lo = (nan_bytes(vf[2 * h][w]) >> (8 * e)) & 1u, hi = (nan_bytes(vf[2 * h + 1][w]) >> (8 * e)) & 1u;
                         one[h] = (lo ? 0x3c00u : 0u) | (hi ? 0x3c000000u : 0u);
                     }
                     float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -360,17 +381,24 @@ __global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const Att
                         if (c[i] > 0.0f) o[4 * w + e][i] = __int_as_float(0x7fffffff);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f.v[i][w] &= ~nan_bytes(f.v[i][w]);
+                for (int i = 0; i < 4; ++i) vf[i][w] &= ~nan_bytes(vf[i][w]);
             }
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-            const uint32_t lo0 = __byte_perm(f.v[0][w], f.v[1][w], 0x5140), hi0 = __byte_perm(f.v[0][w], f.v[1][w], 0x7362);
-            const uint32_t lo1 = __byte_perm(f.v[2][w], f.v[3][w], 0x5140), hi1 = __byte_perm(f.v[2][w], f.v[3][w], 0x7362);
+            const uint32_t lo0 = __byte_perm(vf[0][w], vf[1][w], 0x5140), hi0 = __byte_perm(vf[0][w], vf[1][w], 0x7362);
+            const uint32_t lo1 = __byte_perm(vf[2][w], vf[3][w], 0x5140), hi1 = __byte_perm(vf[2][w], vf[3][w], 0x7362);
             mma_f16(o[4 * w], p0, p1, p2, p3, e4m3x2_f16x2(lo0), e4m3x2_f16x2(lo1));
             mma_f16(o[4 * w + 1], p0, p1, p2, p3, e4m3x2_f16x2(lo0 >> 16), e4m3x2_f16x2(lo1 >> 16));
             mma_f16(o[4 * w + 2], p0, p1, p2, p3, e4m3x2_f16x2(hi0), e4m3x2_f16x2(hi1));
             mma_f16(o[4 * w + 3], p0, p1, p2, p3, e4m3x2_f16x2(hi0 >> 16), e4m3x2_f16x2(hi1 >> 16));
+        }
+        // every lane has its codes: the stage takes the step S turns on
+        __syncwarp();
+        if (lane == 0 && st + S * kWarps < steps) fetch(st + S * kWarps, stage);
+        if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
         }
     }
 
@@ -385,7 +413,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const Att
         red_l[warp][g] = l0;
         red_l[warp][g + 8] = l1;
     }
-    __syncthreads();  // also: every warp is done with the page ids
+    __syncthreads();  // also: every warp is done with its ring
     float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -437,13 +465,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps<D>) attn_rows_kernel(const Att
     }
 }
 
-// Joins the splits of a row: one warp per row.
+// Joins the splits of a row: one CTA per row, its four warps take turns of the
+// splits, four at a time.
 template <int D>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, const AttnSplit sp) {
+    __shared__ float part[4][D + 2];
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t u = blockIdx.x;
     const float* slots = sp.ws + u * sp.splits * kAttnSlot<D>;
     const int64_t in_tile = u % sp.slot_rows;
     u /= sp.slot_rows;
@@ -451,33 +481,63 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, cons
     u /= sp.row_tiles;
     const int hk = (int)(u % p.c.heads);
     const int64_t b = u / p.c.heads;
-    if (b >= p.batch) return;
     const AttnSeq s = attn_seq(p, b, false);
     if (row >= s.n * p.group) return;
     // the splits that its row tile filled (the first always)
     const int64_t last = min64(s.n * p.group, (row / kAttnRows + 1) * kAttnRows) - 1;
     const int64_t most = attn_limit(p, s, last);
     const int n = most > sp.chunk ? (int)((most + sp.chunk - 1) / sp.chunk) : 1;
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, slots[i * kAttnSlot<D> + D]);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    float l = 0.0f, v[D / 32];
+    float top = -INFINITY, l = 0.0f, v[D / 32];
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) v[d] = 0.0f;
-    for (int i = 0; i < n; ++i) {
-        const float* slot = slots + i * kAttnSlot<D>;
-        const float m = slot[D], a = m == -INFINITY ? 1.0f : exp2_approx(m - top);
-        l = fmaf(slot[D + 1], a, l);
+    for (int i0 = warp; i0 < n; i0 += 16) {
+        float m[4], z[4], x[4][D / 32];
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) v[d] = fmaf(slot[lane * (D / 32) + d], a, v[d]);
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + 4 * k;
+            const float* slot = slots + min(i, n - 1) * kAttnSlot<D>;
+            m[k] = i < n ? slot[D] : -INFINITY;
+            z[k] = i < n ? slot[D + 1] : 0.0f;
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) x[k][d] = i < n ? slot[lane * (D / 32) + d] : 0.0f;
+        }
+        const float t4 = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
+        const float keep = top == -INFINITY ? 1.0f : exp2_approx(top - t4);  // (nothing, or NaN, so far)
+        l *= keep;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) v[d] *= keep;
+        top = t4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float a = m[k] == -INFINITY ? 1.0f : exp2_approx(m[k] - top);
+            l = fmaf(z[k], a, l);
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) v[d] = fmaf(x[k][d], a, v[d]);
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) part[warp][lane * (D / 32) + d] = v[d];
+    if (lane == 0) {
+        part[warp][D] = top;
+        part[warp][D + 1] = l;
+    }
+    __syncthreads();
+    if (threadIdx.x >= D / 2) return;
+    top = fmaxf(fmaxf(part[0][D], part[1][D]), fmaxf(part[2][D], part[3][D]));
+    const int d = 2 * threadIdx.x;
+    float x0 = 0.0f, x1 = 0.0f;
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float a = part[w][D] == -INFINITY ? 1.0f : exp2_approx(part[w][D] - top);
+        l = fmaf(part[w][D + 1], a, l);
+        x0 = fmaf(part[w][d], a, x0);
+        x1 = fmaf(part[w][d + 1], a, x1);
     }
     const int64_t tok = s.first + row / p.group, h = (int64_t)hk * p.group + row % p.group;
     const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + lane * (D / 32));
-#pragma unroll
-    for (int d = 0; d < D / 32; d += 2) dst[d / 2] = bf16x2_pack(v[d] * inv, v[d + 1] * inv);
-    if (p.lse && lane == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+    *reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + d) = bf16x2_pack(x0 * inv, x1 * inv);
+    if (p.lse && threadIdx.x == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
 }  // namespace fp4q

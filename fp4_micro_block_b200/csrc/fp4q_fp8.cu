@@ -292,7 +292,7 @@ fp4q_status attn_plan(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_h
     if (a.row_tiles >= kMaxDim / kv_heads || a.row_tiles * kv_heads >= kMaxDim / batch) return FP4Q_ERR_UNSUPPORTED;
     a.slot_rows = std::min<int64_t>(kAttnRows, max_q * (q_heads / kv_heads));
     const int64_t items = batch * kv_heads * a.row_tiles;
-    const int64_t want = std::max<int64_t>(1, spans(6 * (int64_t)sms, items));
+    const int64_t want = std::max<int64_t>(1, spans(3 * (int64_t)sms, items));
     a.chunk = std::min<int64_t>(kAttnMaxChunk, std::max<int64_t>(128, spans(spans(max_len, want), 128) * 128));
     a.splits = std::max<int64_t>(1, spans(max_len, a.chunk));
     if (a.splits >= kMaxDim / items || items >= kMaxDim / kAttnRows) return FP4Q_ERR_UNSUPPORTED;
@@ -301,13 +301,36 @@ fp4q_status attn_plan(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_h
     return FP4Q_OK;
 }
 
+// One side of a cache as [pages * heads * page_size, head_dim] codes, in boxes of
+// 16 rows x min(head_dim, 128) bytes (swizzled by the box's width).
+fp4q_status make_kv_map(CUtensorMap* map, const KvCacheView& c, const uint8_t* codes) {
+    EncodeTiledFn enc;
+    fp4q_status st = encode_fn(&enc);
+    if (st != FP4Q_OK) return st;
+    cuuint64_t dims[2] = {(cuuint64_t)c.dim, (cuuint64_t)(c.num_pages * c.heads * c.page)};
+    cuuint64_t strides[1] = {(cuuint64_t)c.dim};
+    cuuint32_t box[2] = {(cuuint32_t)std::min(c.dim, 128), (cuuint32_t)kAttnStep};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, c.dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FP4Q_OK : FP4Q_ERR_CUDA;
+}
+
 template <int D>
 fp4q_status launch_attn(const AttnParams& p, const AttnPlan& a, void* ws, cudaStream_t s) {
+    using G = AttnGeo<D>;
     AttnSplit sp{a.row_tiles, a.splits, a.chunk, (int32_t)a.slot_rows, a.splits > 1 ? static_cast<float*>(ws) : nullptr};
+    auto kern = attn_rows_kernel<D>;
+    static std::atomic<uint64_t> done{0};
+    fp4q_status st = ensure_smem(kern, G::smem, done);
+    if (st != FP4Q_OK) return st;
+    CUtensorMap map_k, map_v;
+    if ((st = make_kv_map(&map_k, p.c, p.c.k)) != FP4Q_OK || (st = make_kv_map(&map_v, p.c, p.c.v)) != FP4Q_OK) return st;
     const int64_t items = p.batch * p.c.heads * a.row_tiles;
-    fp4q_status st = launch(attn_rows_kernel<D>, (int)(items * a.splits), 32 * kAttnWarps<D>, 0, s, p, sp);
+    st = launch(kern, (int)(items * a.splits), 32 * G::warps, G::smem, s, map_k, map_v, p, sp);
     if (st != FP4Q_OK || a.splits == 1) return st;
-    return launch(attn_join_kernel<D>, (int)spans(items * a.slot_rows, 4), 128, 0, s, p, sp);
+    return launch(attn_join_kernel<D>, (int)(items * a.slot_rows), 128, 0, s, p, sp);
 }
 
 }  // namespace
