@@ -57,9 +57,9 @@ __device__ __forceinline__ int64_t attn_page(const AttnParams& p, int64_t b, int
 // ------------------------------------------------------------------ few queries
 //
 // One CTA: one sequence, one K/V head, 16 rows (query i, head g of the group:
-// row i * G + g) and one run of keys; four warps take turns of 16 keys, which
-// lie within one page.  Decoding is bound by reading the cache: each warp keeps a
-// ring of such steps on its way (TMA boxes of 16 rows, swizzled so that the reads
+// row i * G + g) and one run of keys; four warps take turns of 32 keys, two tiles
+// of 16 that lie within a page each.  Decoding is bound by reading the cache: each warp keeps a
+// ring of such tiles on its way (TMA boxes of 16 rows, swizzled so that the reads
 // below have no bank conflicts), and lanes read whole 16-byte pieces of codes:
 // which of a product's k (or n) indices a lane's bytes stand for is free as long
 // as both operands agree.
@@ -118,7 +118,7 @@ __device__ __forceinline__ int attn_limit(const AttnParams& p, const AttnSeq& s,
     return i < s.n && lim > 0 ? (int)lim : 0;
 }
 
-// A step's codes of K or V in shared memory: boxes of 16 rows x min(D, 128)
+// A tile's codes of K or V in shared memory: boxes of 16 rows x min(D, 128)
 // bytes, whose 16-byte pieces the TMA's swizzle permutes within a row.
 template <int D>
 struct AttnTile {
@@ -156,21 +156,55 @@ __device__ __forceinline__ void ld_words(uint32_t (&w)[N], const uint8_t* tile, 
 template <int D>
 struct AttnGeo {
     static constexpr int warps = 4;
-    static constexpr int stages = D == 256 ? 3 : 4;
+    static constexpr int stages = D == 64 ? 3 : 2;                // turns (two tiles) on their way per warp
     static constexpr int ctas = D == 256 ? 1 : D == 128 ? 3 : 4;  // per SM, for the register budget
-    static constexpr int stage_bytes = 2 * AttnTile<D>::bytes;
+    static constexpr int tile_bytes = 2 * AttnTile<D>::bytes;     // K and V
+    static constexpr int stage_bytes = 2 * tile_bytes;
     static constexpr int ring = warps * stages * stage_bytes;
     static constexpr int pages = kAttnMaxChunk / 16;
     static constexpr int red = warps * kAttnRows * (D + 4) * 4;  // the warps' sums, in the ring's place
     static constexpr int qf_off = ring > red ? ring : red;
     static constexpr int ids_off = qf_off + D / 16 * 32 * 16;
-    static constexpr int ml_off = ids_off + 3 * 4 * pages;
+    static constexpr int ml_off = ids_off + 4 * 4 * pages;
     static constexpr int bar_off = ml_off + 2 * 4 * warps * kAttnRows;
     static constexpr int smem = 1024 + bar_off + 8 * warps * stages;
 };
 
 // Bytes of w that are NaN codes, as 0xff; the others 0.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
+// A NaN code of V reaches the rows that see its key and no other: it is taken out
+// of the product (vf), and the rows that see one are counted with products of 0s
+// and 1s.  key: the lane's first key; limits of rows g and g + 8.
+template <int D>
+__device__ __forceinline__ void attn_take_nans(uint32_t (&vf)[4][D / 32], float (&o)[D / 8][4], int64_t key, int lim0, int lim1) {
+    uint32_t see[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // row g, row g + 8 of keys 2t, 2t + 1; then of keys 8 + 2t, 9 + 2t
+        const int64_t kk = key + 8 * (i >> 1);
+        const int lim = (i & 1) ? lim1 : lim0;
+        see[i] = (kk < lim ? 0x3c00u : 0u) | (kk + 1 < lim ? 0x3c000000u : 0u);
+    }
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t one[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t lo = (nan_bytes(vf[2 * h][w]) >> (8 * e)) & 1u, hi = (nan_bytes(vf[2 * h + 1][w]) >> (8 * e)) & 1u;
+                one[h] = (lo ? 0x3c00u : 0u) | (hi ? 0x3c000000u : 0u);
+            }
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma_f16(c, see[0], see[1], see[2], see[3], one[0], one[1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c[i] > 0.0f) o[4 * w + e][i] = __int_as_float(0x7fffffff);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vf[i][w] &= ~nan_bytes(vf[i][w]);
+    }
+}
 
 template <int D>
 __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
@@ -183,7 +217,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
     float* red = reinterpret_cast<float*>(smem);
     uint4(*qf)[32] = reinterpret_cast<uint4(*)[32]>(smem + G::qf_off);  // the queries as fragments, for every warp
     int32_t* ids = reinterpret_cast<int32_t*>(smem + G::ids_off);       // the split's pages: row / page, scales
-    float *ks = reinterpret_cast<float*>(ids + G::pages), *vs = ks + G::pages;
+    float *ks = reinterpret_cast<float*>(ids + G::pages), *vs = ks + G::pages, *lvs = vs + G::pages;
     float(*red_m)[kAttnRows] = reinterpret_cast<float(*)[kAttnRows]>(smem + G::ml_off);
     float(*red_l)[kAttnRows] = red_m + kWarps;
     pdl_wait();
@@ -214,6 +248,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
         ids[i] = (int32_t)at;
         ks[i] = p.c.k_scale[at] * p.scale_log2;
         vs[i] = p.c.v_scale[at];
+        lvs[i] = log2f(fmaxf(vs[i], 0x1p-100f));  // scales below 2^-100 (and 0) weigh as 2^-100 in the maximum only
     }
 
     // this lane's part of the queries: rows g and g + 8, dims D/4 t .. D/4 t + D/4 - 1, scaled by a power of two
@@ -256,78 +291,97 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
     for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
 
-    const int steps = k0 < k1 ? (int)((k1 - k0 + kAttnStep - 1) / kAttnStep) : 0;
+    const int tiles = k0 < k1 ? (int)((k1 - k0 + kAttnStep - 1) / kAttnStep) : 0;
+    const int turns = (tiles + 1) / 2;
     const int per_page = p.c.page / kAttnStep, shift = per_page == 1 ? 0 : per_page == 2 ? 1 : per_page == 4 ? 2 : 3;
     uint8_t* ring = smem + warp * (S * G::stage_bytes);
     const uint32_t full0 = smem_u32(smem + G::bar_off) + 8 * S * warp;
-    auto fetch = [&](int st, int stage) {  // one lane
-        const uint32_t dst = smem_u32(ring + stage * G::stage_bytes), bar = full0 + 8 * stage;
-        const int32_t row = ids[st >> shift] * p.c.page + (st & (per_page - 1)) * kAttnStep;
-        mbar_arrive_expect_tx(bar, G::stage_bytes);
+    auto fetch = [&](int turn, int stage) {  // one lane
+        const uint32_t bar = full0 + 8 * stage;
+        const int n = min(2, tiles - 2 * turn);
+        mbar_arrive_expect_tx(bar, n * G::tile_bytes);
+        for (int j = 0; j < n; ++j) {
+            const int tile = 2 * turn + j;
+            const int32_t row = ids[tile >> shift] * p.c.page + (tile & (per_page - 1)) * kAttnStep;
+            const uint32_t dst = smem_u32(ring + stage * G::stage_bytes + j * G::tile_bytes);
 #pragma unroll
-        for (int c = 0; c < D; c += AttnTile<D>::box_cols) {
-            tma_load_2d(dst + c * kAttnStep, &map_k, c, row, bar);
-            tma_load_2d(dst + AttnTile<D>::bytes + c * kAttnStep, &map_v, c, row, bar);
+            for (int c = 0; c < D; c += AttnTile<D>::box_cols) {
+                tma_load_2d(dst + c * kAttnStep, &map_k, c, row, bar);
+                tma_load_2d(dst + AttnTile<D>::bytes + c * kAttnStep, &map_v, c, row, bar);
+            }
         }
     };
     if (lane == 0) {
         for (int i = 0; i < S; ++i) mbar_init(full0 + 8 * i, 1);
         fence_barrier_init();
-        for (int i = 0; i < S && warp + i * kWarps < steps; ++i) fetch(warp + i * kWarps, i);
+        for (int i = 0; i < S && warp + i * kWarps < turns; ++i) fetch(warp + i * kWarps, i);
     }
     __syncwarp();
     int stage = 0;
     uint32_t phase = 0;
 #pragma unroll 1
-    for (int st = warp; st < steps; st += kWarps) {
+    for (int turn = warp; turn < turns; turn += kWarps) {
         if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * stage, phase))) {
             if (lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
             break;
         }
-        const uint8_t *kt = ring + stage * G::stage_bytes, *vt = kt + AttnTile<D>::bytes;
-        // codes of this lane: keys g, 8 + g of K; 2t, 2t+1, 8+2t, 9+2t of V
-        uint32_t kf[2][D / 16], vf[4][D / 32];
-        ld_words<D>(kf[0], kt, g, t * (D / 4));
-        ld_words<D>(kf[1], kt, g + 8, t * (D / 4));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ld_words<D>(vf[i], vt, 2 * t + (i & 1) + 8 * (i >> 1), g * (D / 8));
-        const int page = st >> shift;
-        const int64_t key = k0 + (int64_t)st * kAttnStep;
-        const float kscale = ks[page], vscale = vs[page];
+        // The last turn may have one tile: what lies in the other's place is of
+        // keys that no row sees.
+        const uint8_t* at = ring + stage * G::stage_bytes;
+        const int64_t key = k0 + (int64_t)turn * (2 * kAttnStep);
+        const int page[2] = {(2 * turn) >> shift, min(2 * turn + 1, tiles - 1) >> shift};
 
-        float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // keys 2t, 2t+1; 8 + 2t, ...
+        float sc[2][2][4] = {};  // [tile][keys 2t, 2t+1 / 8+2t, 9+2t][row g: 0, 1; row g + 8: 2, 3]
+        {
+            uint32_t kf[2][2][KW];  // codes of this lane: keys g, 8 + g
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-            const uint4 a = qf[w][lane];
-            mma_f16(s0, a.x, a.y, a.z, a.w, e4m3x2_f16x2(kf[0][w]), e4m3x2_f16x2(kf[0][w] >> 16));
-            mma_f16(s1, a.x, a.y, a.z, a.w, e4m3x2_f16x2(kf[1][w]), e4m3x2_f16x2(kf[1][w] >> 16));
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) ld_words<D>(kf[j][i], at + j * G::tile_bytes, g + 8 * i, t * (D / 4));
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+                const uint4 a = qf[w][lane];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const Half4 k = e4m3x4_f16(kf[j][i][w]);
+                        mma_f16(sc[j][i], a.x, a.y, a.z, a.w, k.lo, k.hi);
+                    }
+            }
         }
-        const float f0 = kscale * qs[0], f1 = kscale * qs[1];
-        float x[8] = {s0[0] * f0, s0[1] * f0, s1[0] * f0, s1[1] * f0, s0[2] * f1, s0[3] * f1, s1[2] * f1, s1[3] * f1};
-        bool nans = false;
-        if (key + kAttnStep > every) {  // some row does not see some key of this step
+        float x[2][8];  // [tile][row g: keys 2t, 2t+1, 8+2t, 9+2t; row g + 8: the same]
+        float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float f = ks[page[j]], f0 = f * qs[0], f1 = f * qs[1];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t kk = key + 2 * t + (i & 1) + 8 * (i >> 1);
-                if (kk >= lim0) x[i] = -INFINITY;
-                if (kk >= lim1) x[4 + i] = -INFINITY;
-                uint32_t any = 0;
-#pragma unroll
-                for (int w = 0; w < D / 32; ++w) {
-                    if (kk >= most) vf[i][w] = 0;  // beyond the last row's keys: whatever lies there
-                    any |= nan_bytes(vf[i][w]);
-                }
-                nans = nans || any != 0;
+                x[j][i] = sc[j][i >> 1][i & 1] * f0;
+                x[j][4 + i] = sc[j][i >> 1][2 + (i & 1)] * f1;
             }
-            nans = __any_sync(0xffffffffu, nans);
         }
-        // log2 of the V scale; scales below 2^-100 (and 0) weigh as 2^-100 in the maximum only
-        const float lv = log2f(fmaxf(vscale, 0x1p-100f));
-        float t0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), t1 = fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]));
+        const bool edge = key + 2 * kAttnStep > every;  // some row does not see some key of this turn
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t kk = key + kAttnStep * j + 2 * t + (i & 1) + 8 * (i >> 1);
+                    if (kk >= lim0) x[j][i] = -INFINITY;
+                    if (kk >= lim1) x[j][4 + i] = -INFINITY;
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float lv = lvs[page[j]];
+            t0 = fmaxf(t0, fmaxf(fmaxf(x[j][0], x[j][1]), fmaxf(x[j][2], x[j][3])) + lv);
+            t1 = fmaxf(t1, fmaxf(fmaxf(x[j][4], x[j][5]), fmaxf(x[j][6], x[j][7])) + lv);
+        }
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2)) + lv;
-        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2)) + lv;
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
         if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {
             const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
             const float a0 = n0 == -INFINITY ? 1.0f : exp2_approx(m0 - n0), a1 = n1 == -INFINITY ? 1.0f : exp2_approx(m1 - n1);
@@ -345,57 +399,48 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
         }
         const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] = exp2_approx(x[i] - b0);
-            x[4 + i] = exp2_approx(x[4 + i] - b1);
-            l0 += x[i];
-            l1 += x[4 + i];
-        }
-        const float wv = vscale * 0x1p14f;
-        const uint32_t p0 = f16x2_pack(x[0] * wv, x[1] * wv), p1 = f16x2_pack(x[4] * wv, x[5] * wv),
-                       p2 = f16x2_pack(x[2] * wv, x[3] * wv), p3 = f16x2_pack(x[6] * wv, x[7] * wv);
-        if (nans) {
-            // A NaN code of V reaches the rows that see its key and no other: it is
-            // taken out of the product, and the rows that see one are counted.
-            uint32_t see[4];
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // a0: row g, a1: row g + 8 of keys 2t, 2t + 1; a2, a3: of keys 8 + 2t, ...
-                const int64_t kk = key + 2 * t + 8 * (i >> 1);
-                const int lim = (i & 1) ? lim1 : lim0;
-                see[i] = (kk < lim ? 0x3c00u : 0u) | (kk + 1 < lim ? 0x3c000000u : 0u);
+            for (int i = 0; i < 4; ++i) {
+                x[j][i] = exp2_approx(x[j][i] - b0);
+                x[j][4 + i] = exp2_approx(x[j][4 + i] - b1);
+                l0 += x[j][i];
+                l1 += x[j][4 + i];
+            }
+            const float wv = vs[page[j]] * 0x1p14f;
+            const uint32_t p0 = f16x2_pack(x[j][0] * wv, x[j][1] * wv), p1 = f16x2_pack(x[j][4] * wv, x[j][5] * wv),
+                           p2 = f16x2_pack(x[j][2] * wv, x[j][3] * wv), p3 = f16x2_pack(x[j][6] * wv, x[j][7] * wv);
+            uint32_t vf[4][D / 32];  // codes of this lane: keys 2t, 2t+1, 8+2t, 9+2t
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ld_words<D>(vf[i], at + j * G::tile_bytes + AttnTile<D>::bytes, 2 * t + (i & 1) + 8 * (i >> 1), g * (D / 8));
+            if (edge) {
+                const int64_t tk = key + kAttnStep * j;
+                bool nans = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool dead = tk + 2 * t + (i & 1) + 8 * (i >> 1) >= most;
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w) {
+                        if (dead) vf[i][w] = 0;  // beyond the last row's keys: whatever lies there
+                        nans = nans || nan_bytes(vf[i][w]) != 0;
+                    }
+                }
+                if (__any_sync(0xffffffffu, nans)) attn_take_nans<D>(vf, o, tk + 2 * t, lim0, lim1);
             }
 #pragma unroll
             for (int w = 0; w < D / 32; ++w) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t one[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t lo = (nan_bytes(vf[2 * h][w]) >> (8 * e)) & 1u, hi = (nan_bytes(vf[2 * h + 1][w]) >> (8 * e)) & 1u;
-                        one[h] = (lo ? 0x3c00u : 0u) | (hi ? 0x3c000000u : 0u);
-                    }
-                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma_f16(c, see[0], see[1], see[2], see[3], one[0], one[1]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (c[i] > 0.0f) o[4 * w + e][i] = __int_as_float(0x7fffffff);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) vf[i][w] &= ~nan_bytes(vf[i][w]);
+                const Half4 a = e4m3x4_f16(__byte_perm(vf[0][w], vf[1][w], 0x5140)), b = e4m3x4_f16(__byte_perm(vf[2][w], vf[3][w], 0x5140));
+                const Half4 c = e4m3x4_f16(__byte_perm(vf[0][w], vf[1][w], 0x7362)), d = e4m3x4_f16(__byte_perm(vf[2][w], vf[3][w], 0x7362));
+                mma_f16(o[4 * w], p0, p1, p2, p3, a.lo, b.lo);
+                mma_f16(o[4 * w + 1], p0, p1, p2, p3, a.hi, b.hi);
+                mma_f16(o[4 * w + 2], p0, p1, p2, p3, c.lo, d.lo);
+                mma_f16(o[4 * w + 3], p0, p1, p2, p3, c.hi, d.hi);
             }
         }
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-            const uint32_t lo0 = __byte_perm(vf[0][w], vf[1][w], 0x5140), hi0 = __byte_perm(vf[0][w], vf[1][w], 0x7362);
-            const uint32_t lo1 = __byte_perm(vf[2][w], vf[3][w], 0x5140), hi1 = __byte_perm(vf[2][w], vf[3][w], 0x7362);
-            mma_f16(o[4 * w], p0, p1, p2, p3, e4m3x2_f16x2(lo0), e4m3x2_f16x2(lo1));
-            mma_f16(o[4 * w + 1], p0, p1, p2, p3, e4m3x2_f16x2(lo0 >> 16), e4m3x2_f16x2(lo1 >> 16));
-            mma_f16(o[4 * w + 2], p0, p1, p2, p3, e4m3x2_f16x2(hi0), e4m3x2_f16x2(hi1));
-            mma_f16(o[4 * w + 3], p0, p1, p2, p3, e4m3x2_f16x2(hi0 >> 16), e4m3x2_f16x2(hi1 >> 16));
-        }
-        // every lane has its codes: the stage takes the step S turns on
+        // every lane has its codes: the stage takes the turn S turns on
         __syncwarp();
-        if (lane == 0 && st + S * kWarps < steps) fetch(st + S * kWarps, stage);
+        if (lane == 0 && turn + S * kWarps < turns) fetch(turn + S * kWarps, stage);
         if (++stage == S) {
             stage = 0;
             phase ^= 1;

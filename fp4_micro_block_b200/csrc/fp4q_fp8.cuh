@@ -26,10 +26,15 @@ __device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float 
     return w;
 }
 
-// Two E4M3 codes (the halves' low byte first) as an f16 pair (exact).
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
-    uint32_t h;
-    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l; }" : "=r"(h) : "r"(two));
+// Four E4M3 codes as two f16 pairs (exact).
+struct Half4 {
+    uint32_t lo, hi;
+};
+__device__ __forceinline__ Half4 e4m3x4_f16(uint32_t four) {
+    Half4 h;
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+        : "=r"(h.lo), "=r"(h.hi)
+        : "r"(four));
     return h;
 }
 
