@@ -25,7 +25,8 @@ constexpr float kLn2 = 0.693147180559945309f;
 
 // Rows and keys of sequence b, clamped to what exists; reports what it clamps.
 struct AttnSeq {
-    int64_t first, n, len;
+    int64_t first;
+    int32_t n, len;  // (rows and keys of a call are counted in 31 bits)
 };
 __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int64_t b, bool tell) {
     AttnSeq s;
@@ -39,14 +40,14 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int64_t b, bool
     }
     if (bad && tell) atomicOr(&g_device_error, kErrBadIndex);
     s.first = lo;
-    s.n = hi - lo;
-    s.len = len;
+    s.n = (int32_t)(hi - lo);
+    s.len = (int32_t)len;
     return s;
 }
 
 // Page id of the sequence's page pg, clamped into the pool.
-__device__ __forceinline__ int64_t attn_page(const AttnParams& p, int64_t b, int64_t pg, bool tell) {
-    int64_t id = p.c.table[b * p.c.table_stride + pg];
+__device__ __forceinline__ int32_t attn_page(const AttnParams& p, int64_t b, int32_t pg, bool tell) {
+    int32_t id = p.c.table[b * p.c.table_stride + pg];
     if (id < 0 || id >= p.c.num_pages) {
         if (tell) atomicOr(&g_device_error, kErrBadIndex);
         id = 0;
@@ -105,17 +106,17 @@ constexpr int kAttnRows = 16, kAttnStep = 16;
 constexpr int kAttnMaxChunk = 4096;   // keys of one split: its pages' ids and scales are in shared memory
 
 struct AttnSplit {
-    int64_t row_tiles, splits;
-    int64_t chunk;      // keys per split, a multiple of 128
-    int32_t slot_rows;  // rows of a tile that may exist: min(16, max_q * G)
+    uint32_t row_tiles, splits;
+    int32_t chunk;      // keys per split, a multiple of 128
+    uint32_t slot_rows; // rows of a tile that may exist: min(16, max_q * G)
     float* ws;          // NULL: one split
 };
 
 // Smallest v such that keys >= v of the row are masked.
-__device__ __forceinline__ int attn_limit(const AttnParams& p, const AttnSeq& s, int64_t r) {
-    const int64_t i = r / p.group;
-    const int64_t lim = p.causal ? s.len - s.n + i + 1 : s.len;
-    return i < s.n && lim > 0 ? (int)lim : 0;
+__device__ __forceinline__ int attn_limit(const AttnParams& p, const AttnSeq& s, int32_t r) {
+    const int32_t i = (int32_t)((uint32_t)r / (uint32_t)p.group);
+    const int32_t lim = p.causal ? s.len - s.n + i + 1 : s.len;
+    return i < s.n && lim > 0 ? lim : 0;
 }
 
 // A tile's codes of K or V in shared memory: boxes of 16 rows x min(D, 128)
@@ -177,11 +178,11 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w &
 // of the product (vf), and the rows that see one are counted with products of 0s
 // and 1s.  key: the lane's first key; limits of rows g and g + 8.
 template <int D>
-__device__ __forceinline__ void attn_take_nans(uint32_t (&vf)[4][D / 32], float (&o)[D / 8][4], int64_t key, int lim0, int lim1) {
+__device__ __forceinline__ void attn_take_nans(uint32_t (&vf)[4][D / 32], float (&o)[D / 8][4], int key, int lim0, int lim1) {
     uint32_t see[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // row g, row g + 8 of keys 2t, 2t + 1; then of keys 8 + 2t, 9 + 2t
-        const int64_t kk = key + 8 * (i >> 1);
+        const int kk = key + 8 * (i >> 1);
         const int lim = (i & 1) ? lim1 : lim0;
         see[i] = (kk < lim ? 0x3c00u : 0u) | (kk + 1 < lim ? 0x3c000000u : 0u);
     }
@@ -220,31 +221,62 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
     float *ks = reinterpret_cast<float*>(ids + G::pages), *vs = ks + G::pages, *lvs = vs + G::pages;
     float(*red_m)[kAttnRows] = reinterpret_cast<float(*)[kAttnRows]>(smem + G::ml_off);
     float(*red_l)[kAttnRows] = red_m + kWarps;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    uint8_t* ring = smem + warp * (S * G::stage_bytes);
+    const uint32_t full0 = smem_u32(smem + G::bar_off) + 8 * S * warp;
+    if (lane == 0) {
+        prefetch_tmap(&map_k);
+        prefetch_tmap(&map_v);
+        for (int i = 0; i < S; ++i) mbar_init(full0 + 8 * i, 1);
+        fence_barrier_init();
+    }
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    int64_t u = blockIdx.x;
-    const int64_t split = u % sp.splits;
+    uint32_t u = blockIdx.x;  // (32-bit divisions: each 64-bit one here costs a tenth of a microsecond)
+    const uint32_t split = u % sp.splits;
     u /= sp.splits;
-    const int64_t rt = u % sp.row_tiles;
+    const uint32_t rt = u % sp.row_tiles;
     u /= sp.row_tiles;
-    const int hk = (int)(u % p.c.heads);
-    const int64_t b = u / p.c.heads;
+    const int hk = (int)(u % (uint32_t)p.c.heads);
+    const int64_t b = u / (uint32_t)p.c.heads;
     const AttnSeq s = attn_seq(p, b, threadIdx.x == 0);
-    const int64_t r0 = rt * kAttnRows;
-    const int64_t rows = min64(s.n * p.group - r0, kAttnRows);
+    const int r0 = (int)rt * kAttnRows;
+    const int rows = min(s.n * p.group - r0, kAttnRows);
     if (rows <= 0) return;
     // keys this tile sees (the last row sees most), and this split's part of them
-    const int64_t most = attn_limit(p, s, r0 + rows - 1);
-    const int64_t k0 = split * sp.chunk, k1 = min64(most, k0 + sp.chunk);
+    const int most = attn_limit(p, s, r0 + rows - 1);
+    const int k0 = (int)min64((int64_t)split * sp.chunk, most), k1 = min(most - k0, sp.chunk) + k0;
     if (split > 0 && k0 >= k1) return;
-    const int64_t every = attn_limit(p, s, r0);  // keys below are seen by every row of the tile
+    const int every = attn_limit(p, s, r0);  // keys below are seen by every row of the tile
     const int lim0 = attn_limit(p, s, r0 + g), lim1 = attn_limit(p, s, r0 + g + 8);
 
-    // page ids and scales of the split
-    const int n_pages = k0 < k1 ? (int)((k1 - k0 + p.c.page - 1) / p.c.page) : 0;
+    // a tile is 16 keys, a turn of a warp two tiles
+    const int tiles = k0 < k1 ? (int)((k1 - k0 + kAttnStep - 1) / kAttnStep) : 0;
+    const int turns = (tiles + 1) / 2;
+    const int per_page = p.c.page / kAttnStep, shift = per_page == 1 ? 0 : per_page == 2 ? 1 : per_page == 4 ? 2 : 3;
+    auto fetch = [&](int turn, int stage, auto&& id) {  // one lane
+        const uint32_t bar = full0 + 8 * stage;
+        const int n = min(2, tiles - 2 * turn);
+        mbar_arrive_expect_tx(bar, n * G::tile_bytes);
+        for (int j = 0; j < n; ++j) {
+            const int tile = 2 * turn + j;
+            const int32_t row = id(tile >> shift) * p.c.page + (tile & (per_page - 1)) * kAttnStep;
+            const uint32_t dst = smem_u32(ring + stage * G::stage_bytes + j * G::tile_bytes);
+#pragma unroll
+            for (int c = 0; c < D; c += AttnTile<D>::box_cols) {
+                tma_load_2d(dst + c * kAttnStep, &map_k, c, row, bar);
+                tma_load_2d(dst + AttnTile<D>::bytes + c * kAttnStep, &map_v, c, row, bar);
+            }
+        }
+    };
+    // the first turns' codes are on their way before anything else is known of the pages
+    const int page0 = (k0 / kAttnStep) >> shift;
+    if (lane == 0)
+        for (int i = 0; i < S && warp + i * kWarps < turns; ++i)
+            fetch(warp + i * kWarps, i, [&](int pg) { return (int32_t)(attn_page(p, b, page0 + pg, false) * p.c.heads + hk); });
+    const int n_pages = (tiles + per_page - 1) >> shift;
     for (int i = threadIdx.x; i < n_pages; i += 32 * kWarps) {
-        const int64_t at = attn_page(p, b, k0 / p.c.page + i, true) * p.c.heads + hk;
+        const int64_t at = attn_page(p, b, page0 + i, true) * p.c.heads + hk;
         ids[i] = (int32_t)at;
         ks[i] = p.c.k_scale[at] * p.scale_log2;
         vs[i] = p.c.v_scale[at];
@@ -255,9 +287,9 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
     float qs[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int64_t r = r0 + g + 8 * i;
-        const bool live = r < s.n * p.group;
-        const uint16_t* src = p.q + (s.first + (live ? r / p.group : 0)) * p.ldq + ((int64_t)hk * p.group + (live ? r % p.group : 0)) * D + t * (D / 4);
+        const bool live = r0 + g + 8 * i < s.n * p.group;
+        const uint32_t r = live ? r0 + g + 8 * i : 0, tok = r / (uint32_t)p.group, h = hk * p.group + (r - tok * p.group);
+        const uint16_t* src = p.q + (s.first + tok) * p.ldq + (int64_t)h * D + t * (D / 4);
         uint4 x[D / 32];
         float amax = 0.0f;
 #pragma unroll
@@ -291,32 +323,6 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
     for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
 
-    const int tiles = k0 < k1 ? (int)((k1 - k0 + kAttnStep - 1) / kAttnStep) : 0;
-    const int turns = (tiles + 1) / 2;
-    const int per_page = p.c.page / kAttnStep, shift = per_page == 1 ? 0 : per_page == 2 ? 1 : per_page == 4 ? 2 : 3;
-    uint8_t* ring = smem + warp * (S * G::stage_bytes);
-    const uint32_t full0 = smem_u32(smem + G::bar_off) + 8 * S * warp;
-    auto fetch = [&](int turn, int stage) {  // one lane
-        const uint32_t bar = full0 + 8 * stage;
-        const int n = min(2, tiles - 2 * turn);
-        mbar_arrive_expect_tx(bar, n * G::tile_bytes);
-        for (int j = 0; j < n; ++j) {
-            const int tile = 2 * turn + j;
-            const int32_t row = ids[tile >> shift] * p.c.page + (tile & (per_page - 1)) * kAttnStep;
-            const uint32_t dst = smem_u32(ring + stage * G::stage_bytes + j * G::tile_bytes);
-#pragma unroll
-            for (int c = 0; c < D; c += AttnTile<D>::box_cols) {
-                tma_load_2d(dst + c * kAttnStep, &map_k, c, row, bar);
-                tma_load_2d(dst + AttnTile<D>::bytes + c * kAttnStep, &map_v, c, row, bar);
-            }
-        }
-    };
-    if (lane == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(full0 + 8 * i, 1);
-        fence_barrier_init();
-        for (int i = 0; i < S && warp + i * kWarps < turns; ++i) fetch(warp + i * kWarps, i);
-    }
-    __syncwarp();
     int stage = 0;
     uint32_t phase = 0;
 #pragma unroll 1
@@ -328,7 +334,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
         // The last turn may have one tile: what lies in the other's place is of
         // keys that no row sees.
         const uint8_t* at = ring + stage * G::stage_bytes;
-        const int64_t key = k0 + (int64_t)turn * (2 * kAttnStep);
+        const int key = k0 + turn * (2 * kAttnStep);
         const int page[2] = {(2 * turn) >> shift, min(2 * turn + 1, tiles - 1) >> shift};
 
         float sc[2][2][4] = {};  // [tile][keys 2t, 2t+1 / 8+2t, 9+2t][row g: 0, 1; row g + 8: 2, 3]
@@ -367,7 +373,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int64_t kk = key + kAttnStep * j + 2 * t + (i & 1) + 8 * (i >> 1);
+                    const int kk = key + kAttnStep * j + 2 * t + (i & 1) + 8 * (i >> 1);
                     if (kk >= lim0) x[j][i] = -INFINITY;
                     if (kk >= lim1) x[j][4 + i] = -INFINITY;
                 }
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
             for (int i = 0; i < 4; ++i)
                 ld_words<D>(vf[i], at + j * G::tile_bytes + AttnTile<D>::bytes, 2 * t + (i & 1) + 8 * (i >> 1), g * (D / 8));
             if (edge) {
-                const int64_t tk = key + kAttnStep * j;
+                const int tk = key + kAttnStep * j;
                 bool nans = false;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -440,7 +446,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
         }
         // every lane has its codes: the stage takes the turn S turns on
         __syncwarp();
-        if (lane == 0 && turn + S * kWarps < turns) fetch(turn + S * kWarps, stage);
+        if (lane == 0 && turn + S * kWarps < turns) fetch(turn + S * kWarps, stage, [&](int pg) { return ids[pg]; });
         if (++stage == S) {
             stage = 0;
             phase ^= 1;
@@ -490,9 +496,8 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) v[d] += red[(w * kAttnRows + r) * (D + 4) + lane * (D / 32) + d];
         }
-        const int64_t row = r0 + r;
         if (sp.ws) {
-            float* slot = sp.ws + ((((b * p.c.heads + hk) * sp.row_tiles + rt) * sp.slot_rows + r) * sp.splits + split) * kAttnSlot<D>;
+            float* slot = sp.ws + ((((int64_t)(b * p.c.heads + hk) * sp.row_tiles + rt) * sp.slot_rows + r) * sp.splits + split) * kAttnSlot<D>;
 #pragma unroll
             for (int d = 0; d < D / 32; ++d) slot[lane * (D / 32) + d] = v[d];
             if (lane == 0) {
@@ -500,7 +505,8 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
                 slot[D + 1] = l;
             }
         } else {
-            const int64_t tok = s.first + row / p.group, h = (int64_t)hk * p.group + row % p.group;
+            const uint32_t row = r0 + r, i = row / (uint32_t)p.group;
+            const int64_t tok = s.first + i, h = hk * p.group + (row - i * p.group);
             const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
             uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + lane * (D / 32));
 #pragma unroll
@@ -518,20 +524,20 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, cons
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t u = blockIdx.x;
-    const float* slots = sp.ws + u * sp.splits * kAttnSlot<D>;
-    const int64_t in_tile = u % sp.slot_rows;
+    uint32_t u = blockIdx.x;
+    const float* slots = sp.ws + (int64_t)u * sp.splits * kAttnSlot<D>;
+    const uint32_t in_tile = u % sp.slot_rows;
     u /= sp.slot_rows;
-    const int64_t row = u % sp.row_tiles * kAttnRows + in_tile;
+    const int row = (int)(u % sp.row_tiles * kAttnRows + in_tile);
     u /= sp.row_tiles;
-    const int hk = (int)(u % p.c.heads);
-    const int64_t b = u / p.c.heads;
+    const int hk = (int)(u % (uint32_t)p.c.heads);
+    const int64_t b = u / (uint32_t)p.c.heads;
     const AttnSeq s = attn_seq(p, b, false);
     if (row >= s.n * p.group) return;
     // the splits that its row tile filled (the first always)
-    const int64_t last = min64(s.n * p.group, (row / kAttnRows + 1) * kAttnRows) - 1;
-    const int64_t most = attn_limit(p, s, last);
-    const int n = most > sp.chunk ? (int)((most + sp.chunk - 1) / sp.chunk) : 1;
+    const int last = min(s.n * p.group, (row / kAttnRows + 1) * kAttnRows) - 1;
+    const int most = attn_limit(p, s, last);
+    const int n = most > sp.chunk ? (most - 1) / sp.chunk + 1 : 1;
     float top = -INFINITY, l = 0.0f, v[D / 32];
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) v[d] = 0.0f;
@@ -579,7 +585,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, cons
         x0 = fmaf(part[w][d], a, x0);
         x1 = fmaf(part[w][d + 1], a, x1);
     }
-    const int64_t tok = s.first + row / p.group, h = (int64_t)hk * p.group + row % p.group;
+    const uint32_t i = (uint32_t)row / (uint32_t)p.group;
+    const int64_t tok = s.first + i, h = hk * p.group + (row - i * p.group);
     const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
     *reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + d) = bf16x2_pack(x0 * inv, x1 * inv);
     if (p.lse && threadIdx.x == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;

@@ -284,10 +284,13 @@ struct AttnPlan {
     size_t ws_bytes;
 };
 
+constexpr int64_t kAttnMost = (int64_t)1 << 30;
+
 fp4q_status attn_plan(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_heads, int64_t kv_heads, int64_t dim,
                       int sms, AttnPlan* out) {
     AttnPlan a{};
-    if (max_q >= kMaxDim / (q_heads / kv_heads)) return FP4Q_ERR_UNSUPPORTED;
+    // rows and keys are counted in 31 bits, with room for the last tile
+    if (max_len > kAttnMost || max_q > kAttnMost / (q_heads / kv_heads)) return FP4Q_ERR_UNSUPPORTED;
     a.row_tiles = spans(max_q * (q_heads / kv_heads), kAttnRows);
     if (a.row_tiles >= kMaxDim / kv_heads || a.row_tiles * kv_heads >= kMaxDim / batch) return FP4Q_ERR_UNSUPPORTED;
     a.slot_rows = std::min<int64_t>(kAttnRows, max_q * (q_heads / kv_heads));
@@ -320,7 +323,7 @@ fp4q_status make_kv_map(CUtensorMap* map, const KvCacheView& c, const uint8_t* c
 template <int D>
 fp4q_status launch_attn(const AttnParams& p, const AttnPlan& a, void* ws, cudaStream_t s) {
     using G = AttnGeo<D>;
-    AttnSplit sp{a.row_tiles, a.splits, a.chunk, (int32_t)a.slot_rows, a.splits > 1 ? static_cast<float*>(ws) : nullptr};
+    AttnSplit sp{(uint32_t)a.row_tiles, (uint32_t)a.splits, (int32_t)a.chunk, (uint32_t)a.slot_rows, a.splits > 1 ? static_cast<float*>(ws) : nullptr};
     auto kern = attn_rows_kernel<D>;
     static std::atomic<uint64_t> done{0};
     fp4q_status st = ensure_smem(kern, G::smem, done);

@@ -409,7 +409,8 @@ fp4q_status fp4q_kv_append_fp8(const void* k, int64_t ldk, const void* v, int64_
  *   cu_q     int32 [batch + 1]: sequence b's queries are rows cu_q[b] .. cu_q[b + 1] - 1.
  *   lens     int32 [batch]: cached tokens of sequence b (the queries' own
  *            included, written before by fp4q_kv_append_fp8).
- *   max_q, max_len  no sequence has more queries / cached tokens than these.
+ *   max_q, max_len  no sequence has more queries / cached tokens than these
+ *            (max_q * G and max_len at most 2^30).
  *   causal   1: query i of n sees keys j <= lens[b] - n + i; 0: all lens[b] keys.
  *   o        bf16 [tokens, num_q_heads, head_dim], token stride ldo (multiple of 8).
  *   lse      float [tokens, num_q_heads], the natural logarithm of the sum of
