@@ -45,6 +45,19 @@ fp4q_status check_fp8(const void* codes, int64_t rows, int64_t cols, int64_t ld,
     return FP4Q_OK;
 }
 
+template <bool TILE>
+fp4q_status launch_fp8_tile(const Fp8QuantParams& p, cudaStream_t s) {
+    auto kern = fp8_tile_kernel<TILE>;
+    static std::atomic<uint64_t> done{0};
+    int sms = 0;
+    fp4q_status st;
+    if ((st = sm_count(&sms)) != FP4Q_OK || (st = ensure_smem(kern, kFp8TileSmem, done)) != FP4Q_OK) return st;
+    CUtensorMap map;
+    if ((st = make_x_map(&map, p.x, p.M, p.K, p.ldx, kFp8Block)) != FP4Q_OK) return st;
+    const int grid = (int)std::min<int64_t>(p.n_items, (int64_t)kFp8TileCtas * sms);
+    return launch(kern, grid, kFp8TileThreads, kFp8TileSmem, s, map, p);
+}
+
 // Codes [rows, K] with row stride ld, boxes of 128 columns x box_rows with the
 // 128-byte swizzle; columns past K and rows past `rows` read as zero codes.
 fp4q_status make_f8_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, int64_t ld, uint32_t box_rows) {
@@ -199,15 +212,14 @@ FP4Q_API fp4q_status fp4q_quantize_fp8(const void* x, int64_t M, int64_t K, int6
         int sms = 0;
         if ((st = sm_count(&sms)) != FP4Q_OK) return st;
         p.n_items = M * p.n_kb;
+        if (p.n_items >= kMaxDim) return FP4Q_ERR_UNSUPPORTED;
         const int64_t per = kFp8RowThreads / 16;
         const int grid = (int)std::min<int64_t>(spans(p.n_items, per), (int64_t)sms * 8);
         return launch(fp8_row_kernel, grid, kFp8RowThreads, 0, (cudaStream_t)stream, p);
     }
     p.n_items = spans(M, kFp8Block) * p.n_kb;
     if (p.n_items >= kMaxDim) return FP4Q_ERR_UNSUPPORTED;
-    if (block == FP4Q_FP8_TILE)
-        return launch(fp8_tile_kernel<true>, (int)p.n_items, kFp8TileThreads, 0, (cudaStream_t)stream, p);
-    return launch(fp8_tile_kernel<false>, (int)p.n_items, kFp8TileThreads, 0, (cudaStream_t)stream, p);
+    return block == FP4Q_FP8_TILE ? launch_fp8_tile<true>(p, (cudaStream_t)stream) : launch_fp8_tile<false>(p, (cudaStream_t)stream);
 }
 
 FP4Q_API fp4q_status fp4q_gemm_fp8(const uint8_t* a_codes, int64_t lda, const float* a_scales, int64_t ldas,
@@ -268,10 +280,14 @@ FP4Q_API fp4q_status fp4q_kv_append_fp8(const void* k, int64_t ldk, const void* 
     p.cu = cu_new;
     p.lens = lens;
     p.max_new = max_new;
-    p.pages_per_seq = (max_new + p.c.page - 2) / p.c.page + 1;
-    if (p.pages_per_seq * batch >= kMaxDim / (2 * p.c.heads)) return FP4Q_ERR_UNSUPPORTED;
-    return launch(kv_append_kernel, (int)(2 * p.c.heads * p.pages_per_seq * batch), kKvThreads, 0,
-                  (cudaStream_t)stream, p);
+    const int64_t pages = (max_new + p.c.page - 2) / p.c.page + 1;
+    if (pages * batch >= kMaxDim / (2 * p.c.heads)) return FP4Q_ERR_UNSUPPORTED;
+    p.pages_per_seq = (uint32_t)pages;
+    p.per_row_log2 = p.c.dim == 64 ? 3 : p.c.dim == 128 ? 4 : 5;
+    // threads for a page's rows, or for the few that a sequence can bring
+    const int64_t pieces = std::min<int64_t>(p.c.page, max_new) << p.per_row_log2;
+    const int threads = (int)std::min<int64_t>(kKvMaxThreads, std::max<int64_t>(spans(pieces, kKvPieces * 32) * 32, std::min<int64_t>(64, spans(pieces, 32) * 32)));
+    return launch(kv_append_kernel, (int)(2 * p.c.heads * pages * batch), threads, 0, (cudaStream_t)stream, p);
 }
 
 namespace {

@@ -7,7 +7,7 @@
 // the transpose run down the columns, so a CTA holds a whole 128 x 128 tile.
 #pragma once
 
-#include "fp4q_device.cuh"
+#include "fp4q_unit.cuh"
 
 namespace fp4q {
 
@@ -38,20 +38,75 @@ __device__ __forceinline__ Half4 e4m3x4_f16(uint32_t four) {
     return h;
 }
 
-// Block scale and the reciprocal that its quotients use: inv = RN(1/s) where
-// div_rn's preconditions hold for every |x| <= amax, else 0 (IEEE division).
-struct Fp8Scale {
-    float s, inv;
+// A pair of fp32 values and operations on both (each rounded as alone).
+__device__ __forceinline__ uint64_t f2_pack(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_both(float v) { return f2_pack(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Block scale s = amax / 448 and, where div_split's preconditions hold for every
+// |x| <= amax, the negated parts of its split reciprocal (else nrz = 0: IEEE
+// divisions).
+struct __align__(16) Fp8Scale {
+    float s, nrn, nrz, nlo;
 };
 __device__ __forceinline__ Fp8Scale fp8_scale(float amax) {
     Fp8Scale r;
     r.s = __fdiv_rn(amax, kE4m3Max);
-    r.inv = div_fast_ok(r.s, amax) ? __frcp_rn(r.s) : 0.0f;
+    r.nrn = r.nrz = r.nlo = 0.0f;
+    if (div_fast_ok(r.s, amax)) {
+        const Rcp c = make_rcp(r.s);
+        r.nrn = -c.rn;
+        r.nrz = -c.rz;
+        r.nlo = -c.lo;
+    }
     return r;
 }
-__device__ __forceinline__ float fp8_quot(float x, const Fp8Scale& f) {
-    if (f.inv != 0.0f) return div_rn(x, f.s, f.inv);
-    return f.s == 0.0f ? 0.0f : __fdiv_rn(x, f.s);
+__device__ __noinline__ uint32_t fp8_codes_ieee(uint32_t u0, uint32_t u1, float s) {
+    if (s == 0.0f) return 0u;
+    return e4m3_pack4(__fdiv_rn(bf16lo(u0), s), __fdiv_rn(bf16hi(u0), s), __fdiv_rn(bf16lo(u1), s), __fdiv_rn(bf16hi(u1), s));
+}
+// The four codes of two words of bf16 pairs: x / s as div_split computes it,
+// two elements an instruction.
+__device__ __forceinline__ uint32_t fp8_codes(uint32_t u0, uint32_t u1, const Fp8Scale& f) {
+    if (f.nrz == 0.0f) return fp8_codes_ieee(u0, u1, f.s);
+    uint32_t q[4];
+    const uint32_t u[2] = {u0 ^ 0x80008000u, u1 ^ 0x80008000u};  // -x
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint64_t nx = f2_pack(u[i] << 16, u[i] & 0xffff0000u);
+        const uint64_t q0 = f2_fma(nx, f2_both(f.nrz), f2_mul(nx, f2_both(f.nlo)));
+        const uint64_t e = f2_fma(q0, f2_both(f.s), nx);
+        const uint64_t r = f2_fma(e, f2_both(f.nrn), q0);
+        q[2 * i] = (uint32_t)r;
+        q[2 * i + 1] = (uint32_t)(r >> 32);
+    }
+    return e4m3_pack4(__uint_as_float(q[0]), __uint_as_float(q[1]), __uint_as_float(q[2]), __uint_as_float(q[3]));
+}
+
+// Maxima of bf16 magnitudes, two at a time; a NaN loses to a number.
+__device__ __forceinline__ uint32_t bf16x2_abs(uint32_t u) { return u & 0x7fff7fffu; }
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// One number's larger half (NaN only if both are: counts as 0).
+__device__ __forceinline__ float bf16x2_top(uint32_t u) { return fmaxf(fmaxf(bf16lo(u), bf16hi(u)), 0.0f); }
+__device__ __forceinline__ uint32_t amax8x2(const uint4& w) {
+    return bf16x2_max(bf16x2_max(bf16x2_abs(w.x), bf16x2_abs(w.y)), bf16x2_max(bf16x2_abs(w.z), bf16x2_abs(w.w)));
 }
 
 struct Fp8QuantParams {
@@ -96,154 +151,197 @@ __device__ __forceinline__ void fp8_store8(uint8_t* dst, uint32_t lo, uint32_t h
         if (i < n) dst[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
 }
 
-__device__ __forceinline__ float amax8(const uint4& w) {
-    const float a = fmaxf(fmaxf(fabsf(bf16lo(w.x)), fabsf(bf16hi(w.x))), fmaxf(fabsf(bf16lo(w.y)), fabsf(bf16hi(w.y))));
-    const float b = fmaxf(fmaxf(fabsf(bf16lo(w.z)), fabsf(bf16hi(w.z))), fmaxf(fabsf(bf16lo(w.w)), fabsf(bf16hi(w.w))));
-    return fmaxf(a, b);
-}
+__device__ __forceinline__ float amax8(const uint4& w) { return bf16x2_top(amax8x2(w)); }
 
 // Row blocks alone: 16 lanes hold one 1 x 128 block, eight elements each.
 constexpr int kFp8RowThreads = 256;
 __global__ void __launch_bounds__(kFp8RowThreads) fp8_row_kernel(const Fp8QuantParams p) {
     pdl_wait();
     pdl_trigger();
-    const int lane16 = threadIdx.x & 15;
-    const int64_t step = (int64_t)gridDim.x * (kFp8RowThreads / 16);
-    const int64_t first = (int64_t)blockIdx.x * (kFp8RowThreads / 16) + (threadIdx.x >> 4);
-    // both halves of a warp make the same number of trips (the shuffles' lanes)
-    for (int64_t base = first & ~1ll; base < p.n_items; base += step) {
-        const int64_t i = base + (first & 1);
-        const int64_t r = i / p.n_kb, kb = i - r * p.n_kb;
-        const int64_t c = kb * kFp8Block + lane16 * 8;
-        const uint4 w = i < p.n_items ? fp8_load8(p, r, c) : make_uint4(0, 0, 0, 0);
+    const uint32_t lane16 = threadIdx.x & 15, n_kb = (uint32_t)p.n_kb;
+    const uint32_t half = (threadIdx.x >> 4) & 1, step = gridDim.x * (kFp8RowThreads / 16);
+    // (row, block) of this half-warp, which moves on by `step` blocks; both halves
+    // of a warp make the same number of trips (the shuffles' lanes)
+    const uint32_t first = blockIdx.x * (kFp8RowThreads / 16) + (threadIdx.x >> 4);
+    uint32_t r = first / n_kb, kb = first - r * n_kb;
+    const uint32_t dr = step / n_kb, dkb = step - dr * n_kb;
+    for (int64_t base = first - half; base < p.n_items; base += step) {
+        const bool live = base + half < p.n_items;
+        const int64_t c = (int64_t)kb * kFp8Block + lane16 * 8;
+        const uint4 w = live ? fp8_load8(p, r, c) : make_uint4(0, 0, 0, 0);
         float amax = amax8(w);
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (i >= p.n_items) continue;
-        const Fp8Scale f = fp8_scale(amax);
-        if (c < p.K)
-            fp8_store8(p.codes + r * p.ldc + c,
-                       e4m3_pack4(fp8_quot(bf16lo(w.x), f), fp8_quot(bf16hi(w.x), f), fp8_quot(bf16lo(w.y), f),
-                                  fp8_quot(bf16hi(w.y), f)),
-                       e4m3_pack4(fp8_quot(bf16lo(w.z), f), fp8_quot(bf16hi(w.z), f), fp8_quot(bf16lo(w.w), f),
-                                  fp8_quot(bf16hi(w.w), f)),
-                       p.K - c);
-        if (lane16 == 0) p.scales[kb * p.lds + r] = f.s;
+        if (live) {
+            const Fp8Scale f = fp8_scale(amax);
+            if (c < p.K) fp8_store8(p.codes + r * p.ldc + c, fp8_codes(w.x, w.y, f), fp8_codes(w.z, w.w, f), p.K - c);
+            if (lane16 == 0) p.scales[kb * p.lds + r] = f.s;
+        }
+        r += dr;
+        kb += dkb;
+        if (kb >= n_kb) {
+            kb -= n_kb;
+            ++r;
+        }
     }
 }
 
-// One 128 x 128 tile per CTA, held in registers: thread (rg, cl) has rows
-// 8 rg .. 8 rg + 7, columns 8 cl .. 8 cl + 7, so that a row's 128 columns are
-// the 16 lanes of a half-warp (coalesced loads and stores, row maxima by
-// shuffles) and a column's eight rows are one 8-byte piece of the transpose.
-// Those pieces cross the CTA through 16 KiB of shared memory whose 8-byte units
-// are swizzled by the column group, so that neither side has bank conflicts.
+// A 128 x 128 tile at a time, for the transpose and for tile scales: TMA brings
+// the next tile (two boxes of 64 columns, 128-byte swizzle) while this one is
+// worked on.  Thread (rg, cl) has rows 8 rg .. 8 rg + 7, columns 8 cl .. 8 cl + 7,
+// so that a row's 128 columns are the 16 lanes of a half-warp (whole 128-byte
+// runs of codes, row maxima by shuffles, two rows packed in a word) and a
+// column's eight rows are one 8-byte piece of the transpose.  Those pieces cross
+// the CTA through 16 KiB of shared memory whose 8-byte units are swizzled by the
+// column group, so that neither side has bank conflicts.
 constexpr int kFp8TileThreads = 256;
+constexpr int kFp8TileBytes = 2 * kFp8Block * kFp8Block;
+constexpr int kFp8TileStages = 2;
+constexpr int kFp8TurnedOff = kFp8TileStages * kFp8TileBytes;
+constexpr int kFp8PartOff = kFp8TurnedOff + kFp8Block * kFp8Block;
+constexpr int kFp8ColOff = kFp8PartOff + 8 * (kFp8Block / 2) * 4;
+constexpr int kFp8TileBarOff = kFp8ColOff + kFp8Block * 16;
+constexpr int kFp8TileSmem = 1024 + kFp8TileBarOff + 8 * kFp8TileStages;
+constexpr int kFp8TileCtas = 2;  // per SM
+
 template <bool TILE>
-__global__ void __launch_bounds__(kFp8TileThreads) fp8_tile_kernel(const Fp8QuantParams p) {
-    __shared__ __align__(16) uint8_t turned[kFp8Block * kFp8Block];
-    __shared__ float part[8][kFp8Block];
-    __shared__ Fp8Scale col_scale[kFp8Block];
+__global__ void __launch_bounds__(kFp8TileThreads, kFp8TileCtas)
+    fp8_tile_kernel(const __grid_constant__ CUtensorMap map_x, const Fp8QuantParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = align_shared<1024>(smem_raw);
+    uint8_t* turned = smem + kFp8TurnedOff;
+    uint32_t(*part)[kFp8Block / 2] = reinterpret_cast<uint32_t(*)[kFp8Block / 2]>(smem + kFp8PartOff);
+    Fp8Scale* col_scale = reinterpret_cast<Fp8Scale*>(smem + kFp8ColOff);
+    const uint32_t full0 = smem_u32(smem + kFp8TileBarOff);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cl = tid & 15, rg = tid >> 4;
+    if (tid == 0) {
+        prefetch_tmap(&map_x);
+        for (int i = 0; i < kFp8TileStages; ++i) mbar_init(full0 + 8 * i, 1);
+        fence_barrier_init();
+    }
     pdl_wait();
     pdl_trigger();
-    const int64_t mb = blockIdx.x / p.n_kb, kb = blockIdx.x - mb * p.n_kb;
-    const int64_t r0 = mb * kFp8Block + rg * 8, c = kb * kFp8Block + cl * 8;
-    uint4 w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = fp8_load8(p, r0 + i, c);
-
-    Fp8Scale whole;
-    if constexpr (TILE) {
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, amax8(w[i]));
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (lane == 0) part[warp][0] = amax;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, part[i][0]);
-        whole = fp8_scale(amax);
-        if (tid == 0) {
-            if (p.codes) p.scales[kb * p.lds + mb] = whole.s;
-            if (p.codes_t) p.scales_t[mb * p.ldst + kb] = whole.s;
-        }
-    } else if (p.codes_t) {
-        float m[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                m[2 * j] = fmaxf(m[2 * j], fabsf(bf16lo(u[j])));
-                m[2 * j + 1] = fmaxf(m[2 * j + 1], fabsf(bf16hi(u[j])));
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
-        if (lane < 16) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) part[warp][cl * 8 + j] = m[j];
-        }
-        __syncthreads();
-        if (tid < kFp8Block) {
-            float amax = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, part[i][tid]);
-            const Fp8Scale f = fp8_scale(amax);
-            col_scale[tid] = f;
-            if (kb * kFp8Block + tid < p.K) p.scales_t[mb * p.ldst + kb * kFp8Block + tid] = f.s;
-        }
-        __syncthreads();
-    }
-
-    if (p.codes) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            Fp8Scale f;
-            if constexpr (TILE) {
-                f = whole;
-            } else {
-                float amax = amax8(w[i]);
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                f = fp8_scale(amax);
-            }
-            const int64_t r = r0 + i;
-            if (r < p.M && c < p.K)
-                fp8_store8(p.codes + r * p.ldc + c,
-                           e4m3_pack4(fp8_quot(bf16lo(w[i].x), f), fp8_quot(bf16hi(w[i].x), f),
-                                      fp8_quot(bf16lo(w[i].y), f), fp8_quot(bf16hi(w[i].y), f)),
-                           e4m3_pack4(fp8_quot(bf16lo(w[i].z), f), fp8_quot(bf16hi(w[i].z), f),
-                                      fp8_quot(bf16lo(w[i].w), f), fp8_quot(bf16hi(w[i].w), f)),
-                           p.K - c);
-            if (!TILE && cl == 0 && r < p.M) p.scales[kb * p.lds + r] = f.s;
-        }
-    }
-    if (!p.codes_t) return;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const Fp8Scale f = TILE ? whole : col_scale[cl * 8 + j];
-        float q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t u = j < 2 ? w[i].x : j < 4 ? w[i].y : j < 6 ? w[i].z : w[i].w;
-            q[i] = fp8_quot((j & 1) ? bf16hi(u) : bf16lo(u), f);
-        }
-        *reinterpret_cast<uint2*>(turned + (cl * 8 + j) * kFp8Block + ((rg ^ cl) & 15) * 8) =
-            make_uint2(e4m3_pack4(q[0], q[1], q[2], q[3]), e4m3_pack4(q[4], q[5], q[6], q[7]));
-    }
     __syncthreads();
+    const uint32_t n_kb = (uint32_t)p.n_kb, n_items = (uint32_t)p.n_items;
+    auto fetch = [&](uint32_t item, int stage) {  // one thread
+        const uint32_t mb = item / n_kb, kb = item - mb * n_kb;
+        const uint32_t dst = smem_u32(smem + stage * kFp8TileBytes), bar = full0 + 8 * stage;
+        mbar_arrive_expect_tx(bar, kFp8TileBytes);
+        tma_load_2d(dst, &map_x, (int32_t)(kb * kFp8Block), (int32_t)(mb * kFp8Block), bar);
+        tma_load_2d(dst + kFp8TileBytes / 2, &map_x, (int32_t)(kb * kFp8Block + 64), (int32_t)(mb * kFp8Block), bar);
+    };
+    if (tid == 0)
+        for (int i = 0; i < kFp8TileStages; ++i)
+            if (blockIdx.x + i * gridDim.x < n_items) fetch(blockIdx.x + i * gridDim.x, i);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (uint32_t item = blockIdx.x; item < n_items; item += gridDim.x) {
+        if (!__syncthreads_and(mbar_wait(full0 + 8 * stage, phase))) {
+            if (tid == 0) atomicOr(&g_device_error, kErrWaitTimeout);
+            return;
+        }
+        const uint32_t mb = item / n_kb, kb = item - mb * n_kb;
+        const int64_t r0 = (int64_t)mb * kFp8Block + rg * 8, c = (int64_t)kb * kFp8Block + cl * 8;
+        uint4 w[8];
+        const uint8_t* tile = smem + stage * kFp8TileBytes + (cl >> 3) * (kFp8TileBytes / 2);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = i * 16 + (tid >> 4);  // a column of x
-        const int64_t k = kb * kFp8Block + row, m = mb * kFp8Block + cl * 8;
-        const uint2 v = *reinterpret_cast<const uint2*>(turned + row * kFp8Block + ((cl ^ (row >> 3)) & 15) * 8);
-        if (k < p.K && m < p.M) fp8_store8(p.codes_t + k * p.ldct + m, v.x, v.y, p.M - m);
+        for (int i = 0; i < 8; ++i)
+            w[i] = *reinterpret_cast<const uint4*>(tile + (8 * rg + i) * 128 + (((cl & 7) ^ i) << 4));
+
+        Fp8Scale whole;
+        if constexpr (TILE) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = bf16x2_max(m, amax8x2(w[i]));
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) m = bf16x2_max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (lane == 0) part[warp][0] = m;
+        } else if (p.codes_t) {
+            uint32_t m[4] = {0, 0, 0, 0};  // columns 2j, 2j + 1 of the eight
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                m[0] = bf16x2_max(m[0], bf16x2_abs(w[i].x));
+                m[1] = bf16x2_max(m[1], bf16x2_abs(w[i].y));
+                m[2] = bf16x2_max(m[2], bf16x2_abs(w[i].z));
+                m[3] = bf16x2_max(m[3], bf16x2_abs(w[i].w));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m[j] = bf16x2_max(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+            if (lane < 16) *reinterpret_cast<uint4*>(&part[warp][cl * 4]) = make_uint4(m[0], m[1], m[2], m[3]);
+        }
+        __syncthreads();  // the maxima are there, and every thread has its part of the tile
+        if (tid == 0 && item + kFp8TileStages * gridDim.x < n_items) fetch(item + kFp8TileStages * gridDim.x, stage);
+        if (++stage == kFp8TileStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+        if constexpr (TILE) {
+            uint32_t m = part[0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) m = bf16x2_max(m, part[i][0]);
+            whole = fp8_scale(bf16x2_top(m));
+            if (tid == 0) {
+                if (p.codes) p.scales[kb * p.lds + mb] = whole.s;
+                if (p.codes_t) p.scales_t[mb * p.ldst + kb] = whole.s;
+            }
+        } else if (p.codes_t) {
+            if (tid < kFp8Block) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = bf16x2_max(m, part[i][tid >> 1]);
+                const Fp8Scale f = fp8_scale(fmaxf((tid & 1) ? bf16hi(m) : bf16lo(m), 0.0f));
+                col_scale[tid] = f;
+                const int64_t k = (int64_t)kb * kFp8Block + tid;
+                if (k < p.K) p.scales_t[mb * p.ldst + k] = f.s;
+            }
+            __syncthreads();
+        }
+
+        if (p.codes) {
+            uint32_t m[4];  // maxima of rows 2i, 2i + 1 in one word
+            if constexpr (!TILE) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a = amax8x2(w[2 * i]), b = amax8x2(w[2 * i + 1]);
+                    m[i] = bf16x2_max(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) m[i] = bf16x2_max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const Fp8Scale f = TILE ? whole : fp8_scale(fmaxf((i & 1) ? bf16hi(m[i / 2]) : bf16lo(m[i / 2]), 0.0f));
+                const int64_t r = r0 + i;
+                if (r < p.M && c < p.K)
+                    fp8_store8(p.codes + r * p.ldc + c, fp8_codes(w[i].x, w[i].y, f), fp8_codes(w[i].z, w[i].w, f), p.K - c);
+                if (!TILE && cl == 0 && r < p.M) p.scales[kb * p.lds + r] = f.s;
+            }
+        }
+        if (!p.codes_t) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // columns 2j, 2j + 1: their rows two by two
+            uint32_t u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = j == 0 ? w[i].x : j == 1 ? w[i].y : j == 2 ? w[i].z : w[i].w;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const Fp8Scale f = TILE ? whole : col_scale[cl * 8 + 2 * j + h];
+                const uint32_t sel = h ? 0x7632 : 0x5410;
+                *reinterpret_cast<uint2*>(turned + (cl * 8 + 2 * j + h) * kFp8Block + ((rg ^ cl) & 15) * 8) =
+                    make_uint2(fp8_codes(__byte_perm(u[0], u[1], sel), __byte_perm(u[2], u[3], sel), f),
+                               fp8_codes(__byte_perm(u[4], u[5], sel), __byte_perm(u[6], u[7], sel), f));
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = i * 16 + rg;  // a column of x
+            const int64_t k = (int64_t)kb * kFp8Block + row, m = (int64_t)mb * kFp8Block + cl * 8;
+            const uint2 v = *reinterpret_cast<const uint2*>(turned + row * kFp8Block + ((cl ^ (row >> 3)) & 15) * 8);
+            if (k < p.K && m < p.M) fp8_store8(p.codes_t + k * p.ldct + m, v.x, v.y, p.M - m);
+        }
+        // (the next tile's first barrier keeps its maxima and pieces behind these reads)
     }
 }
 

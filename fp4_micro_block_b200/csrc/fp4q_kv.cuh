@@ -36,44 +36,42 @@ __device__ __forceinline__ float kv_inverse(float s) {
     return s == 0.0f ? 0.0f : __uint_as_float((254u << 23) - __float_as_uint(s));
 }
 
-// x / s: an exact product where s is a power of two, as this file writes it; a
-// page may also carry a calibrated scale of the caller's.
-__device__ __forceinline__ float kv_quot(float x, float s, float inv) {
-    return (__float_as_uint(s) & 0x7fffffu) == 0 ? x * inv : __fdiv_rn(x, s);
-}
-
 struct KvAppendParams {
     KvCacheView c;
     const uint16_t *k, *v;
     int64_t ldk, ldv, tokens;
     const int32_t *cu, *lens;
     int64_t max_new;
-    int64_t pages_per_seq;  // pages a sequence's new tokens may touch
+    uint32_t pages_per_seq;  // pages a sequence's new tokens may touch
+    int32_t per_row_log2;    // log2 of the eight-column pieces of a row
 };
 
-// One CTA per (sequence, touched page, head, K or V).  Every step is a pass over
-// the page's rows by all threads, eight columns each.
-constexpr int kKvThreads = 128;
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvAppendParams p) {
-    __shared__ float part[kKvThreads / 32];
+// One CTA per (sequence, touched page, head, K or V).  A thread holds up to
+// kKvPieces pieces of eight columns of the page's new rows between the maximum
+// and the codes; the launch has threads for a whole page.
+constexpr int kKvPieces = 8, kKvMaxThreads = 512;
+__global__ void __launch_bounds__(kKvMaxThreads) kv_append_kernel(const KvAppendParams p) {
+    __shared__ uint32_t part[kKvMaxThreads / 32];
     pdl_wait();
     pdl_trigger();
     const KvCacheView& c = p.c;
-    int64_t i = blockIdx.x;
+    uint32_t i = blockIdx.x;
     const bool is_v = i & 1;
     i >>= 1;
-    const int h = (int)(i % c.heads);
-    i /= c.heads;
-    const int64_t j = i % p.pages_per_seq, b = i / p.pages_per_seq;
+    const int h = (int)(i % (uint32_t)c.heads);
+    i /= (uint32_t)c.heads;
+    const uint32_t b = i / p.pages_per_seq, j = i - b * p.pages_per_seq;
     // the new tokens' rows and positions
     int64_t lo = p.cu[b], hi = p.cu[b + 1];
+    const int64_t end = p.lens[b];
     bool bad = lo < 0 || hi < lo || hi > p.tokens || hi - lo > p.max_new;
     if (bad) hi = lo;
-    const int64_t n = hi - lo, end = p.lens[b], begin = end - n;
+    const int n = (int)(hi - lo);
+    const int64_t begin = end - n;
     bad = bad || begin < 0 || end > c.table_stride * c.page;
-    const int64_t pg = (begin < 0 ? 0 : begin) / c.page + j;  // page index within the sequence
-    const int64_t p0 = pg * c.page;                           // its first position
-    int64_t from = begin > p0 ? begin : p0, to = end < p0 + c.page ? end : p0 + c.page;
+    const int pg = (int)((uint32_t)(bad ? 0 : begin) / (uint32_t)c.page + j);  // page index within the sequence
+    const int64_t p0 = (int64_t)pg * c.page;                                   // its first position
+    const int from = (int)(begin > p0 ? begin - p0 : 0), to = (int)min64(end - p0, c.page);  // rows of the page
     int64_t page = -1;
     if (from < to && !bad) {
         page = c.table[b * c.table_stride + pg];
@@ -82,50 +80,56 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvAppendPar
     if (bad && threadIdx.x == 0) atomicOr(&g_device_error, kErrBadIndex);
     if (bad || from >= to) return;
 
-    const uint16_t* src = is_v ? p.v : p.k;
     const int64_t ld = is_v ? p.ldv : p.ldk;
     uint8_t* codes = (is_v ? c.v : c.k) + (page * c.heads + h) * (int64_t)c.page * c.dim;
     float* scale = (is_v ? c.v_scale : c.k_scale) + page * c.heads + h;
-    const int per_row = c.dim / 8;
-    const int kept = (int)(from - p0);  // rows the page has already
-    const int count = (int)(to - from) * per_row;
-    const uint16_t* rows = src + (lo + from - begin) * ld + (int64_t)h * c.dim;
+    // from: rows the page has already
+    const int count = (to - from) << p.per_row_log2, mask = (1 << p.per_row_log2) - 1;
+    const uint16_t* rows = (is_v ? p.v : p.k) + (lo + (p0 + from - begin)) * ld + (int64_t)h * c.dim;
 
-    float amax = 0.0f;
-    for (int e = threadIdx.x; e < count; e += kKvThreads) {
-        const int r = e / per_row, q = e - r * per_row;
-        amax = fmaxf(amax, amax8(__ldg(reinterpret_cast<const uint4*>(rows + r * ld + q * 8))));
+    const float old = from > 0 ? *scale : 0.0f;
+    uint4 w[kKvPieces];
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < kKvPieces; ++k) {
+        const int e = threadIdx.x + k * blockDim.x;
+        w[k] = make_uint4(0, 0, 0, 0);
+        if (e < count) w[k] = __ldg(reinterpret_cast<const uint4*>(rows + (e >> p.per_row_log2) * ld + (e & mask) * 8));
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
-    const float old = kept > 0 ? *scale : 0.0f;
-    __syncthreads();  // every thread has the old scale before it is replaced
-    for (int w = 0; w < kKvThreads / 32; ++w) amax = fmaxf(amax, part[w]);
-    const float s = fmaxf(old, kv_scale(amax)), inv = kv_inverse(s);
+    for (int k = 0; k < kKvPieces; ++k) m = bf16x2_max(m, amax8x2(w[k]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = bf16x2_max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();  // also: every thread has the old scale before it is replaced
+    for (uint32_t k = 0; k < blockDim.x / 32; ++k) m = bf16x2_max(m, part[k]);
+    const float s = fmaxf(old, kv_scale(bf16x2_top(m))), inv = kv_inverse(s);
     if (threadIdx.x == 0) *scale = s;
-    if (s > old && old > 0.0f) {
+    if (s > old && from > 0) {  // what the page has moves to the new scale (a page of zeros so far: zeros)
         const float ratio = old * inv;
-        for (int e = threadIdx.x; e < kept * per_row; e += kKvThreads) {
+        for (int e = threadIdx.x; e < from << p.per_row_log2; e += blockDim.x) {
             uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)e * 8);
-            const uint2 w = *at;
+            const uint2 x = *at;
             float f[8];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) f[t] = e4m3_decode(((t < 4 ? w.x : w.y) >> (8 * (t & 3)))) * ratio;
-            *at = make_uint2(e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7]));
+            for (int k = 0; k < 8; ++k) f[k] = e4m3_decode(((k < 4 ? x.x : x.y) >> (8 * (k & 3)))) * ratio;
+            *at = old > 0.0f ? make_uint2(e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7])) : make_uint2(0, 0);
         }
-    } else if (s > old) {  // a page of zeros so far
-        for (int e = threadIdx.x; e < kept * per_row; e += kKvThreads)
-            *reinterpret_cast<uint2*>(codes + (int64_t)e * 8) = make_uint2(0, 0);
     }
-    for (int e = threadIdx.x; e < count; e += kKvThreads) {
-        const int r = e / per_row, q = e - r * per_row;
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(rows + r * ld + q * 8));
-        *reinterpret_cast<uint2*>(codes + (int64_t)(kept + r) * c.dim + q * 8) =
-            make_uint2(e4m3_pack4(kv_quot(bf16lo(w.x), s, inv), kv_quot(bf16hi(w.x), s, inv),
-                                  kv_quot(bf16lo(w.y), s, inv), kv_quot(bf16hi(w.y), s, inv)),
-                       e4m3_pack4(kv_quot(bf16lo(w.z), s, inv), kv_quot(bf16hi(w.z), s, inv),
-                                  kv_quot(bf16lo(w.w), s, inv), kv_quot(bf16hi(w.w), s, inv)));
+    const bool exact = (__float_as_uint(s) & 0x7fffffu) == 0;  // a power of two, as this kernel writes it
+#pragma unroll
+    for (int k = 0; k < kKvPieces; ++k) {
+        const int e = threadIdx.x + k * blockDim.x;
+        if (e >= count) break;
+        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+        float f[8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            f[2 * t] = exact ? bf16lo(u[t]) * inv : __fdiv_rn(bf16lo(u[t]), s);
+            f[2 * t + 1] = exact ? bf16hi(u[t]) * inv : __fdiv_rn(bf16hi(u[t]), s);
+        }
+        *reinterpret_cast<uint2*>(codes + ((int64_t)from << (p.per_row_log2 + 3)) + (int64_t)e * 8) =
+            make_uint2(e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7]));
     }
 }
 
