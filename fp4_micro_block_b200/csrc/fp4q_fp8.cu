@@ -211,7 +211,7 @@ FP4Q_API fp4q_status fp4q_quantize_fp8(const void* x, int64_t M, int64_t K, int6
     if (block == FP4Q_FP8_ROW && !codes_t) {
         int sms = 0;
         if ((st = sm_count(&sms)) != FP4Q_OK) return st;
-        p.n_items = M * p.n_kb;
+        p.n_items = spans(M, kFp8RowBlocks) * p.n_kb;
         if (p.n_items >= kMaxDim) return FP4Q_ERR_UNSUPPORTED;
         const int64_t per = kFp8RowThreads / 16;
         const int grid = (int)std::min<int64_t>(spans(p.n_items, per), (int64_t)sms * 8);

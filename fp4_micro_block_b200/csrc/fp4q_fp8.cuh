@@ -74,6 +74,15 @@ __device__ __forceinline__ Fp8Scale fp8_scale(float amax) {
     }
     return r;
 }
+// The scale that lane `src` of the warp holds.
+__device__ __forceinline__ Fp8Scale fp8_scale_of(const Fp8Scale& f, int src) {
+    Fp8Scale r;
+    r.s = __shfl_sync(0xffffffffu, f.s, src);
+    r.nrn = __shfl_sync(0xffffffffu, f.nrn, src);
+    r.nrz = __shfl_sync(0xffffffffu, f.nrz, src);
+    r.nlo = __shfl_sync(0xffffffffu, f.nlo, src);
+    return r;
+}
 __device__ __noinline__ uint32_t fp8_codes_ieee(uint32_t u0, uint32_t u1, float s) {
     if (s == 0.0f) return 0u;
     return e4m3_pack4(__fdiv_rn(bf16lo(u0), s), __fdiv_rn(bf16hi(u0), s), __fdiv_rn(bf16lo(u1), s), __fdiv_rn(bf16hi(u1), s));
@@ -153,35 +162,50 @@ __device__ __forceinline__ void fp8_store8(uint8_t* dst, uint32_t lo, uint32_t h
 
 __device__ __forceinline__ float amax8(const uint4& w) { return bf16x2_top(amax8x2(w)); }
 
-// Row blocks alone: 16 lanes hold one 1 x 128 block, eight elements each.
-constexpr int kFp8RowThreads = 256;
+// Row blocks alone: 16 lanes hold one 1 x 128 block, eight elements each, and
+// four blocks of a K block's neighbouring rows at once; lane i of the 16 works
+// out the scale of block i % 4 for all of them (a division and a reciprocal
+// cost more than a block's codes).
+constexpr int kFp8RowThreads = 256, kFp8RowBlocks = 4;
 __global__ void __launch_bounds__(kFp8RowThreads) fp8_row_kernel(const Fp8QuantParams p) {
     pdl_wait();
     pdl_trigger();
-    const uint32_t lane16 = threadIdx.x & 15, n_kb = (uint32_t)p.n_kb;
+    constexpr int N = kFp8RowBlocks;
+    const uint32_t l16 = threadIdx.x & 15, lane = threadIdx.x & 31, n_kb = (uint32_t)p.n_kb;
     const uint32_t half = (threadIdx.x >> 4) & 1, step = gridDim.x * (kFp8RowThreads / 16);
-    // (row, block) of this half-warp, which moves on by `step` blocks; both halves
-    // of a warp make the same number of trips (the shuffles' lanes)
+    // (rows N r .., block kb) of this half-warp, which moves on by `step` items;
+    // both halves of a warp make the same number of trips (the shuffles' lanes)
     const uint32_t first = blockIdx.x * (kFp8RowThreads / 16) + (threadIdx.x >> 4);
-    uint32_t r = first / n_kb, kb = first - r * n_kb;
+    uint32_t r4 = first / n_kb, kb = first - r4 * n_kb;
     const uint32_t dr = step / n_kb, dkb = step - dr * n_kb;
     for (int64_t base = first - half; base < p.n_items; base += step) {
-        const bool live = base + half < p.n_items;
-        const int64_t c = (int64_t)kb * kFp8Block + lane16 * 8;
-        const uint4 w = live ? fp8_load8(p, r, c) : make_uint4(0, 0, 0, 0);
-        float amax = amax8(w);
+        const int64_t c = (int64_t)kb * kFp8Block + l16 * 8, r0 = (int64_t)r4 * N;
+        uint4 w[N];
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (live) {
-            const Fp8Scale f = fp8_scale(amax);
-            if (c < p.K) fp8_store8(p.codes + r * p.ldc + c, fp8_codes(w.x, w.y, f), fp8_codes(w.z, w.w, f), p.K - c);
-            if (lane16 == 0) p.scales[kb * p.lds + r] = f.s;
+        for (int k = 0; k < N; ++k) w[k] = fp8_load8(p, r0 + k, c);  // zeros past the last row
+        uint32_t m[N / 2];
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {  // two rows' maxima in a word
+            const uint32_t a = amax8x2(w[2 * k]), b = amax8x2(w[2 * k + 1]);
+            m[k] = bf16x2_max(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) m[k] = bf16x2_max(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
         }
-        r += dr;
+        const uint32_t mine = (l16 & 2) ? m[1] : m[0];
+        const Fp8Scale f = fp8_scale(fmaxf((l16 & 1) ? bf16hi(mine) : bf16lo(mine), 0.0f));
+        if (l16 < N && r0 + l16 < p.M) p.scales[kb * p.lds + r0 + l16] = f.s;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const Fp8Scale fk = fp8_scale_of(f, (lane & 16) + k);
+            const int64_t r = r0 + k;
+            if (r < p.M && c < p.K)
+                fp8_store8(p.codes + r * p.ldc + c, fp8_codes(w[k].x, w[k].y, fk), fp8_codes(w[k].z, w[k].w, fk), p.K - c);
+        }
+        r4 += dr;
         kb += dkb;
         if (kb >= n_kb) {
             kb -= n_kb;
-            ++r;
+            ++r4;
         }
     }
 }
@@ -299,8 +323,9 @@ __global__ void __launch_bounds__(kFp8TileThreads, kFp8TileCtas)
         }
 
         if (p.codes) {
-            uint32_t m[4];  // maxima of rows 2i, 2i + 1 in one word
+            Fp8Scale rows;  // !TILE: of row cl % 8 of this half-warp's eight
             if constexpr (!TILE) {
+                uint32_t m[4];  // maxima of rows 2i, 2i + 1 in one word
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t a = amax8x2(w[2 * i]), b = amax8x2(w[2 * i + 1]);
@@ -308,14 +333,16 @@ __global__ void __launch_bounds__(kFp8TileThreads, kFp8TileCtas)
 #pragma unroll
                     for (int o = 1; o < 16; o <<= 1) m[i] = bf16x2_max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
                 }
+                const uint32_t mine = (cl & 4) ? ((cl & 2) ? m[3] : m[2]) : ((cl & 2) ? m[1] : m[0]);
+                rows = fp8_scale(fmaxf((cl & 1) ? bf16hi(mine) : bf16lo(mine), 0.0f));
+                if (cl < 8 && r0 + cl < p.M) p.scales[kb * p.lds + r0 + cl] = rows.s;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const Fp8Scale f = TILE ? whole : fp8_scale(fmaxf((i & 1) ? bf16hi(m[i / 2]) : bf16lo(m[i / 2]), 0.0f));
+                const Fp8Scale f = TILE ? whole : fp8_scale_of(rows, (lane & 16) + i);
                 const int64_t r = r0 + i;
                 if (r < p.M && c < p.K)
                     fp8_store8(p.codes + r * p.ldc + c, fp8_codes(w[i].x, w[i].y, f), fp8_codes(w[i].z, w[i].w, f), p.K - c);
-                if (!TILE && cl == 0 && r < p.M) p.scales[kb * p.lds + r] = f.s;
             }
         }
         if (!p.codes_t) continue;
