@@ -88,9 +88,8 @@ __device__ __noinline__ uint32_t fp8_codes_ieee(uint32_t u0, uint32_t u1, float 
     return e4m3_pack4(__fdiv_rn(bf16lo(u0), s), __fdiv_rn(bf16hi(u0), s), __fdiv_rn(bf16lo(u1), s), __fdiv_rn(bf16hi(u1), s));
 }
 // The four codes of two words of bf16 pairs: x / s as div_split computes it,
-// two elements an instruction.
-__device__ __forceinline__ uint32_t fp8_codes(uint32_t u0, uint32_t u1, const Fp8Scale& f) {
-    if (f.nrz == 0.0f) return fp8_codes_ieee(u0, u1, f.s);
+// two elements an instruction (fp8_codes_fast: f.nrz != 0).
+__device__ __forceinline__ uint32_t fp8_codes_fast(uint32_t u0, uint32_t u1, const Fp8Scale& f) {
     uint32_t q[4];
     const uint32_t u[2] = {u0 ^ 0x80008000u, u1 ^ 0x80008000u};  // -x
 #pragma unroll
@@ -103,6 +102,9 @@ __device__ __forceinline__ uint32_t fp8_codes(uint32_t u0, uint32_t u1, const Fp
         q[2 * i + 1] = (uint32_t)(r >> 32);
     }
     return e4m3_pack4(__uint_as_float(q[0]), __uint_as_float(q[1]), __uint_as_float(q[2]), __uint_as_float(q[3]));
+}
+__device__ __forceinline__ uint32_t fp8_codes(uint32_t u0, uint32_t u1, const Fp8Scale& f) {
+    return f.nrz != 0.0f ? fp8_codes_fast(u0, u1, f) : fp8_codes_ieee(u0, u1, f.s);
 }
 
 // Maxima of bf16 magnitudes, two at a time; a NaN loses to a number.
@@ -300,6 +302,9 @@ __global__ void __launch_bounds__(kFp8TileThreads, kFp8TileCtas)
             stage = 0;
             phase ^= 1;
         }
+        // a whole tile, and scales that the quick quotients take: no tests per piece
+        const bool whole_tile = (int64_t)(mb + 1) * kFp8Block <= p.M && (int64_t)(kb + 1) * kFp8Block <= p.K;
+        bool quick = true, cols_quick = false;
         if constexpr (TILE) {
             uint32_t m = part[0][0];
 #pragma unroll
@@ -309,21 +314,23 @@ __global__ void __launch_bounds__(kFp8TileThreads, kFp8TileCtas)
                 if (p.codes) p.scales[kb * p.lds + mb] = whole.s;
                 if (p.codes_t) p.scales_t[mb * p.ldst + kb] = whole.s;
             }
+            cols_quick = whole.nrz != 0.0f;
         } else if (p.codes_t) {
             if (tid < kFp8Block) {
                 uint32_t m = 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) m = bf16x2_max(m, part[i][tid >> 1]);
                 const Fp8Scale f = fp8_scale(fmaxf((tid & 1) ? bf16hi(m) : bf16lo(m), 0.0f));
-                col_scale[tid] = f;
+                col_scale[(tid & 7) * 16 + (tid >> 3)] = f;  // (read by neighbouring column groups at once)
                 const int64_t k = (int64_t)kb * kFp8Block + tid;
                 if (k < p.K) p.scales_t[mb * p.ldst + k] = f.s;
+                quick = f.nrz != 0.0f;
             }
-            __syncthreads();
+            cols_quick = __syncthreads_and(quick);
         }
 
         if (p.codes) {
-            Fp8Scale rows;  // !TILE: of row cl % 8 of this half-warp's eight
+            Fp8Scale rows{};  // !TILE: of row cl % 8 of this half-warp's eight
             if constexpr (!TILE) {
                 uint32_t m[4];  // maxima of rows 2i, 2i + 1 in one word
 #pragma unroll
@@ -337,36 +344,54 @@ __global__ void __launch_bounds__(kFp8TileThreads, kFp8TileCtas)
                 rows = fp8_scale(fmaxf((cl & 1) ? bf16hi(mine) : bf16lo(mine), 0.0f));
                 if (cl < 8 && r0 + cl < p.M) p.scales[kb * p.lds + r0 + cl] = rows.s;
             }
+            uint8_t* dst = p.codes + r0 * p.ldc + c;
+            if (whole_tile && (TILE ? cols_quick : __all_sync(0xffffffffu, rows.nrz != 0.0f))) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const Fp8Scale f = TILE ? whole : fp8_scale_of(rows, (lane & 16) + i);
-                const int64_t r = r0 + i;
-                if (r < p.M && c < p.K)
-                    fp8_store8(p.codes + r * p.ldc + c, fp8_codes(w[i].x, w[i].y, f), fp8_codes(w[i].z, w[i].w, f), p.K - c);
+                for (int i = 0; i < 8; ++i, dst += p.ldc) {
+                    const Fp8Scale f = TILE ? whole : fp8_scale_of(rows, (lane & 16) + i);
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(fp8_codes_fast(w[i].x, w[i].y, f), fp8_codes_fast(w[i].z, w[i].w, f));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i, dst += p.ldc) {
+                    const Fp8Scale f = TILE ? whole : fp8_scale_of(rows, (lane & 16) + i);
+                    if (r0 + i < p.M && c < p.K)
+                        fp8_store8(dst, fp8_codes(w[i].x, w[i].y, f), fp8_codes(w[i].z, w[i].w, f), p.K - c);
+                }
             }
         }
         if (!p.codes_t) continue;
+        auto turn = [&](auto&& codes) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // columns 2j, 2j + 1: their rows two by two
-            uint32_t u[8];
+            for (int j = 0; j < 4; ++j) {  // columns 2j, 2j + 1: their rows two by two
+                uint32_t u[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = j == 0 ? w[i].x : j == 1 ? w[i].y : j == 2 ? w[i].z : w[i].w;
+                for (int i = 0; i < 8; ++i) u[i] = j == 0 ? w[i].x : j == 1 ? w[i].y : j == 2 ? w[i].z : w[i].w;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const Fp8Scale f = TILE ? whole : col_scale[cl * 8 + 2 * j + h];
-                const uint32_t sel = h ? 0x7632 : 0x5410;
-                *reinterpret_cast<uint2*>(turned + (cl * 8 + 2 * j + h) * kFp8Block + ((rg ^ cl) & 15) * 8) =
-                    make_uint2(fp8_codes(__byte_perm(u[0], u[1], sel), __byte_perm(u[2], u[3], sel), f),
-                               fp8_codes(__byte_perm(u[4], u[5], sel), __byte_perm(u[6], u[7], sel), f));
+                for (int h = 0; h < 2; ++h) {
+                    const Fp8Scale f = TILE ? whole : col_scale[(2 * j + h) * 16 + cl];
+                    const uint32_t sel = h ? 0x7632 : 0x5410;
+                    *reinterpret_cast<uint2*>(turned + (cl * 8 + 2 * j + h) * kFp8Block + ((rg ^ cl) & 15) * 8) =
+                        make_uint2(codes(__byte_perm(u[0], u[1], sel), __byte_perm(u[2], u[3], sel), f),
+                                   codes(__byte_perm(u[4], u[5], sel), __byte_perm(u[6], u[7], sel), f));
+                }
             }
-        }
+        };
+        if (cols_quick)
+            turn([](uint32_t a, uint32_t b, const Fp8Scale& f) { return fp8_codes_fast(a, b, f); });
+        else
+            turn([](uint32_t a, uint32_t b, const Fp8Scale& f) { return fp8_codes(a, b, f); });
         __syncthreads();
+        const int64_t m0 = (int64_t)mb * kFp8Block + cl * 8;
+        uint8_t* dst = p.codes_t + ((int64_t)kb * kFp8Block + rg) * p.ldct + m0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 8; ++i, dst += 16 * p.ldct) {
             const int row = i * 16 + rg;  // a column of x
-            const int64_t k = (int64_t)kb * kFp8Block + row, m = (int64_t)mb * kFp8Block + cl * 8;
             const uint2 v = *reinterpret_cast<const uint2*>(turned + row * kFp8Block + ((cl ^ (row >> 3)) & 15) * 8);
-            if (k < p.K && m < p.M) fp8_store8(p.codes_t + k * p.ldct + m, v.x, v.y, p.M - m);
+            if (whole_tile)
+                *reinterpret_cast<uint2*>(dst) = v;
+            else if ((int64_t)kb * kFp8Block + row < p.K && m0 < p.M)
+                fp8_store8(dst, v.x, v.y, p.M - m0);
         }
         // (the next tile's first barrier keeps its maxima and pieces behind these reads)
     }
