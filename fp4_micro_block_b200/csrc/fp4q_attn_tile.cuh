@@ -1,0 +1,471 @@
+// fp4q_attn_tile.cuh -- the cache attention for many queries: 128 rows (query i,
+// head g of the group: row i * G + g) of one K/V head per CTA on the 5th-generation
+// tensor cores, 128 keys at a time.
+//
+//   S = Q K^T   (128 x 128)  A = Q in tensor memory, B = K as fp16 in shared memory
+//   P = exp2(S - m)          fp16, in tensor memory in S's place
+//   O += P V    (128 x D)    A = P, B = V^T as fp16 in shared memory
+//
+// The codes come as E4M3 by TMA and are converted to fp16 by a warpgroup of
+// their own (exact; V is transposed on the way, so that both products have
+// K-major operands).  Numerics as in fp4q_attn.cuh: the page scales of K and V
+// are applied to S and P, which are fp32 until P is rounded.
+//
+// Warpgroups: 0  warp 0 TMA, warp 1 MMA issue;
+//             1  softmax: thread = row;
+//             2  output: thread = row, O in registers, O = O alpha + P V per tile;
+//             3  conversion.
+// Every wait is bounded; one that runs out sets g_device_error, and the role stops.
+#pragma once
+
+#include "fp4q_attn.cuh"
+#include "fp4q_fp8_gemm.cuh"
+
+namespace fp4q {
+
+constexpr int kTileRows = 128, kTileKeys = 128;
+
+template <int D>
+struct AttnTileGeo {
+    static constexpr int threads = 512;
+    static constexpr int k8 = kTileKeys * D;          // bytes of a tile's K (or V) codes
+    static constexpr int k16 = 2 * kTileKeys * D;     // as fp16
+    static constexpr int raw_off = 0;                 // two stages of K and V codes
+    static constexpr int kf_off = raw_off + 4 * k8;   // two buffers of K, two of V^T
+    static constexpr int vf_off = kf_off + 2 * k16;
+    static constexpr int alpha_off = vf_off + 2 * k16;              // [4][128]
+    static constexpr int ml_off = alpha_off + 4 * kTileRows * 4;    // [2][128]: maxima, denominators
+    static constexpr int nan_off = ml_off + 2 * kTileRows * 4;      // [D]: first key with a NaN in V's column
+    static constexpr int bar_off = nan_off + D * 4;
+    static constexpr int num_bars = 21;
+    static constexpr int slot_off = bar_off + 8 * num_bars;
+    static constexpr int smem = 1024 + slot_off + 16;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    // tensor memory columns
+    static constexpr uint32_t s_col = 0, pv_col = 256, q_col = 384;
+};
+// Registers of the four warpgroups: 4 * 128 at launch.
+constexpr int kTileRegsRoles = 56, kTileRegsSoftmax = 136, kTileRegsOut = 208, kTileRegsConvert = 112;
+static_assert(kTileRegsRoles + kTileRegsSoftmax + kTileRegsOut + kTileRegsConvert == 4 * 128, "register split");
+
+// kind::f16, D fp32, A and B fp16, both K-major, M = 128.
+__host__ __device__ constexpr uint32_t f16_idesc(int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T, K = 16.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Starts the load of 32 consecutive fp32 columns of this thread's TMEM lane; the
+// registers hold them after tmem_wait of the same array.
+__device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+          "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+          "+r"(r[30]), "+r"(r[31])
+        :
+        : "memory");
+}
+// 16 words into this thread's TMEM lane; complete after tmem_wait_st.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(512, 1)
+    attn_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const AttnParams p, const uint32_t row_tiles) {
+    using G = AttnTileGeo<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = align_shared<1024>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2;
+    const uint32_t bars = smem_u32(smem + G::bar_off);
+    const uint32_t full8 = bars, empty8 = bars + 16, kfull = bars + 32, kfree = bars + 48, vfull = bars + 64,
+                   vfree = bars + 80, sfull = bars + 96, pfull = bars + 112, pvfull = bars + 128, pvfree = bars + 136,
+                   qfull = bars + 144, lfull = bars + 152, done_bar = bars + 160;
+    float* alpha = reinterpret_cast<float*>(smem + G::alpha_off);
+    float* ml = reinterpret_cast<float*>(smem + G::ml_off);
+    int* nan_key = reinterpret_cast<int*>(smem + G::nan_off);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::slot_off);
+    if (tid == 0) {
+        prefetch_tmap(&map_k);
+        prefetch_tmap(&map_v);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(full8 + 8 * i, 1);
+            mbar_init(empty8 + 8 * i, 4);
+            mbar_init(kfull + 8 * i, 4);
+            mbar_init(kfree + 8 * i, 1);
+            mbar_init(vfull + 8 * i, 4);
+            mbar_init(vfree + 8 * i, 1);
+            mbar_init(sfull + 8 * i, 1);
+            mbar_init(pfull + 8 * i, 4);
+        }
+        mbar_init(pvfull, 1);
+        mbar_init(pvfree, 4);
+        mbar_init(qfull, 4);
+        mbar_init(lfull, 4);
+        mbar_init(done_bar, 1);
+        fence_barrier_init();
+    }
+    for (int i = tid; i < D; i += 512) nan_key[i] = 0x7fffffff;
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    uint32_t u = blockIdx.x;  // the last row tiles, which see most, first
+    const uint32_t rt = row_tiles - 1 - u % row_tiles;
+    u /= row_tiles;
+    const int hk = (int)(u % (uint32_t)p.c.heads);
+    const int64_t b = u / (uint32_t)p.c.heads;
+    const AttnSeq s = attn_seq(p, b, tid == 0);
+    const int r0 = (int)rt * kTileRows, n_rows = s.n * p.group;
+    const int rows = min(n_rows - r0, kTileRows);
+    const int most = rows > 0 ? attn_limit(p, s, r0 + rows - 1) : 0;  // the last row sees most
+    const int every = rows > 0 ? attn_limit(p, s, r0) : 0;            // keys below are seen by every row
+    const int tiles = (most + kTileKeys - 1) / kTileKeys;
+    const int per_page = p.c.page / kAttnStep, shift = per_page == 1 ? 0 : per_page == 2 ? 1 : per_page == 4 ? 2 : 3;
+
+    if (wg == 0) {
+        reg_dec<kTileRegsRoles>();
+        if (warp == 0) {
+            // -------------------------------------------- TMA: lane i < 8 brings keys 16 i .. of each tile
+            for (int j = 0; j < tiles; ++j) {
+                const int st = j & 1;
+                const int boxes = min(8, (most - j * kTileKeys + kAttnStep - 1) / kAttnStep);
+                const int32_t id = lane < boxes ? attn_page(p, b, (8 * j + lane) >> shift, true) : 0;
+                if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait(empty8 + 8 * st, (uint32_t)(((j >> 1) - 1) & 1)))) {
+                    if (lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(full8 + 8 * st, boxes * 2 * kAttnStep * D);
+                __syncwarp();
+                if (lane < boxes) {
+                    const int32_t row = (id * p.c.heads + hk) * p.c.page + ((8 * j + lane) & (per_page - 1)) * kAttnStep;
+                    const uint32_t dst = smem_u32(smem + G::raw_off) + st * 2 * G::k8 + lane * kAttnStep * D;
+                    tma_load_2d(dst, &map_k, 0, row, full8 + 8 * st);
+                    tma_load_2d(dst + G::k8, &map_v, 0, row, full8 + 8 * st);
+                }
+                __syncwarp();
+            }
+        } else if (warp == 1 && lane == 0 && tiles > 0) {
+            // -------------------------------------------- MMA: S of tile j + 1 goes before P V of tile j
+            bool ok = mbar_wait(qfull, 0);
+            auto issue_s = [&](int j) {
+                const int st = j & 1;
+                ok = ok && mbar_wait(kfull + 8 * st, (uint32_t)((j >> 1) & 1));
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t k = smem_u32(smem + G::kf_off) + st * G::k16;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    umma_f16_ts(tmem + G::s_col + 128 * st, tmem + G::q_col + 8 * i,
+                                sw128_desc(k + (i >> 2) * (kTileKeys * 128) + (i & 3) * 32), f16_idesc(kTileKeys), i > 0);
+                tc_commit(kfree + 8 * st);
+                tc_commit(sfull + 8 * st);
+            };
+            issue_s(0);
+            for (int j = 0; j < tiles && ok; ++j) {
+                if (j + 1 < tiles) issue_s(j + 1);
+                const int st = j & 1;
+                ok = ok && mbar_wait(vfull + 8 * st, (uint32_t)((j >> 1) & 1)) &&
+                     mbar_wait(pfull + 8 * st, (uint32_t)((j >> 1) & 1)) && (j == 0 || mbar_wait(pvfree, (uint32_t)((j - 1) & 1)));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t v = smem_u32(smem + G::vf_off) + st * G::k16;
+#pragma unroll
+                for (int i = 0; i < kTileKeys / 16; ++i)
+                    umma_f16_ts(tmem + G::pv_col, tmem + G::s_col + 128 * st + 8 * i,
+                                sw128_desc(v + (i >> 2) * (D * 128) + (i & 3) * 32), f16_idesc(D), i > 0);
+                tc_commit(vfree + 8 * st);
+                tc_commit(pvfull);
+            }
+            if (!ok) atomicOr(&g_device_error, kErrWaitTimeout);
+            // all MMAs complete before TMEM is freed
+            tc_commit(done_bar);
+            if (!mbar_wait(done_bar, 0)) atomicOr(&g_device_error, kErrWaitTimeout);
+        }
+    } else if (wg == 1) {
+        // ------------------------------------------------ softmax: thread = row
+        reg_inc<kTileRegsSoftmax>();
+        const int t = tid & 127, r = r0 + t;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's TMEM lanes
+        const int lim = rows > 0 ? attn_limit(p, s, r) : 0;
+        float qs = 0.0f;
+        {
+            // the row's query as fp16, scaled by a power of two to a maximum of 2^14, its sign that of the softmax scale
+            const bool live = t < rows;
+            const uint32_t rr = live ? r : 0, tok = rr / (uint32_t)p.group, h = hk * p.group + (rr - tok * p.group);
+            const uint16_t* src = p.q + (s.first + tok) * p.ldq + (int64_t)h * D;
+            uint4 x[D / 8];
+            uint32_t m = 0;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                x[c] = live ? __ldg(reinterpret_cast<const uint4*>(src + 8 * c)) : make_uint4(0, 0, 0, 0);
+                m = bf16x2_max(m, amax8x2(x[c]));
+            }
+            const float amax = bf16x2_top(m);
+            int e = amax == 0.0f ? 0 : 14 + 127 - (int)(__float_as_uint(fmaxf(amax, 0x1p-126f)) >> 23);
+            const int e1 = e / 2, e2 = e - e1;
+            const float u1 = __int_as_float((127 + e1) << 23) * (p.scale_log2 < 0.0f ? -1.0f : 1.0f), u2 = __int_as_float((127 + e2) << 23);
+            qs = __int_as_float((127 - e1) << 23) * __int_as_float((127 - e2) << 23) * fabsf(p.scale_log2);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t q4[4] = {x[4 * c + k].x, x[4 * c + k].y, x[4 * c + k].z, x[4 * c + k].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[4 * k + i] = f16x2_pack(bf16lo(q4[i]) * u1 * u2, bf16hi(q4[i]) * u1 * u2);
+                }
+                tmem_st16(tmem + lanes + G::q_col + 16 * c, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull);
+        }
+        // lanes 0..7: the scales of the next tile's runs of 16 keys
+        float kn = 0.0f, vn = 0.0f;
+        auto scales = [&](int j) {
+            if (lane < 8 && j * kTileKeys + lane * kAttnStep < most) {
+                const int64_t at = attn_page(p, b, (8 * j + lane) >> shift, false) * (int64_t)p.c.heads + hk;
+                kn = __ldg(p.c.k_scale + at);
+                vn = __ldg(p.c.v_scale + at);
+            }
+        };
+        scales(0);
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < tiles; ++j) {
+            const int st = j & 1;
+            const float kv = kn, vv = vn, lv = log2f(fmaxf(vn, 0x1p-100f));
+            if (j + 1 < tiles) scales(j + 1);
+            const int left = lim - j * kTileKeys;  // keys of the tile that this row sees
+            const bool edge = (j + 1) * kTileKeys > every;
+            ok = __all_sync(0xffffffffu, mbar_wait(sfull + 8 * st, (uint32_t)((j >> 1) & 1)));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sa = tmem + lanes + G::s_col + 128 * st;
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kTileKeys / 32; ++c) {
+                uint32_t x[32];
+                tmem_start(sa + 32 * c, x);
+                tmem_wait(x);
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = 32 * c + i < left ? x[i] : 0xff800000u;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float mx = __uint_as_float(x[16 * h]);
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) mx = fmaxf(mx, __uint_as_float(x[16 * h + i]));
+                    const float f = __shfl_sync(0xffffffffu, kv, 2 * c + h) * qs;
+                    top = fmaxf(top, mx * f + __shfl_sync(0xffffffffu, lv, 2 * c + h));  // (-inf * 0 is no number: skipped)
+                }
+            }
+            const float mn = fmaxf(m, top), a = mn == -INFINITY ? 1.0f : exp2_approx(m - mn), base = mn == -INFINITY ? 0.0f : mn;
+            m = mn;
+            l *= a;
+            alpha[(j & 3) * kTileRows + t] = a;
+            // P goes where S was: columns 16 c .. of S's are read by then
+#pragma unroll
+            for (int c = 0; c < kTileKeys / 32; ++c) {
+                uint32_t x[32], w[16];
+                tmem_start(sa + 32 * c, x);
+                tmem_wait(x);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float f = __shfl_sync(0xffffffffu, kv, 2 * c + h) * qs, wv = __shfl_sync(0xffffffffu, vv, 2 * c + h) * 0x1p14f;
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        float e0 = exp2_approx(fmaf(__uint_as_float(x[16 * h + i]), f, -base)), e1 = exp2_approx(fmaf(__uint_as_float(x[16 * h + i + 1]), f, -base));
+                        if (edge) {
+                            e0 = 32 * c + 16 * h + i < left ? e0 : 0.0f;
+                            e1 = 32 * c + 16 * h + i + 1 < left ? e1 : 0.0f;
+                        }
+                        sum += e0 + e1;
+                        w[8 * h + i / 2] = f16x2_pack(e0 * wv, e1 * wv);
+                    }
+                    l += sum;
+                }
+                tmem_st16(sa + 16 * c, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pfull + 8 * st);
+        }
+        if (!ok && lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
+        ml[t] = m;
+        ml[kTileRows + t] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(lfull);
+    } else if (wg == 2) {
+        // ------------------------------------------------ output: thread = row
+        reg_inc<kTileRegsOut>();
+        const int t = tid & 127, r = r0 + t;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        uint64_t o[D / 2];
+#pragma unroll
+        for (int d = 0; d < D / 2; ++d) o[d] = 0;
+        bool ok = true;
+        for (int j = 0; j < tiles; ++j) {
+            ok = __all_sync(0xffffffffu, mbar_wait(pvfull, (uint32_t)(j & 1)));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t a = f2_both(alpha[(j & 3) * kTileRows + t]);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
+                tmem_start(tmem + lanes + G::pv_col + 32 * c, x);
+                tmem_wait(x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[16 * c + i] = f2_fma(o[16 * c + i], a, f2_pack(x[2 * i], x[2 * i + 1]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pvfree);
+        }
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(lfull, 0));
+        if (!ok && lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
+        if (t < rows) {
+            const float m = ml[t], l = ml[kTileRows + t], inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
+            const int lim = attn_limit(p, s, r);
+            const uint32_t tok = (uint32_t)r / (uint32_t)p.group, h = hk * p.group + (r - tok * p.group);
+            uint4* dst = reinterpret_cast<uint4*>(p.o + (s.first + tok) * p.ldo + (int64_t)h * D);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[2 * i] = __uint_as_float((uint32_t)o[4 * c + i]) * inv;
+                    v[2 * i + 1] = __uint_as_float((uint32_t)(o[4 * c + i] >> 32)) * inv;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (nan_key[8 * c + i] < lim) v[i] = __int_as_float(0x7fffffff);
+                dst[c] = make_uint4(bf16x2_pack(v[0], v[1]), bf16x2_pack(v[2], v[3]), bf16x2_pack(v[4], v[5]), bf16x2_pack(v[6], v[7]));
+            }
+            if (p.lse) p.lse[(s.first + tok) * p.q_heads + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+    } else {
+        // ------------------------------------------------ conversion of the codes to fp16
+        reg_dec<kTileRegsConvert>();
+        const int t = tid & 127;
+        bool ok = true;
+        for (int j = 0; j < tiles; ++j) {
+            const int st = j & 1, key0 = j * kTileKeys;
+            const uint32_t ph = (uint32_t)((j >> 1) & 1);
+            ok = mbar_wait(full8 + 8 * st, ph) && (j < 2 || mbar_wait(kfree + 8 * st, ph ^ 1u));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint8_t* raw = smem + G::raw_off + st * 2 * G::k8;
+            const uint32_t kf = smem_u32(smem + G::kf_off) + st * G::k16;
+            // K: eight codes of a key (one 16-byte piece of fp16) at a time
+#pragma unroll 4
+            for (int e = t; e < kTileKeys * D / 8; e += 128) {
+                const int key = e / (D / 8), c = e % (D / 8);
+                const uint2 x = *reinterpret_cast<const uint2*>(raw + (key >> 4) * (kAttnStep * D) + AttnTile<D>::at(key & 15, 8 * c));
+                const Half4 a = e4m3x4_f16(x.x), d = e4m3x4_f16(x.y);
+                sts_v4(kf + (c >> 3) * (kTileKeys * 128) + key * 128 + (((c ^ key) & 7) << 4), a.lo, a.hi, d.lo, d.hi);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(kfull + 8 * st);
+            ok = __all_sync(0xffffffffu, j < 2 || mbar_wait(vfree + 8 * st, ph ^ 1u));
+            if (!ok) break;
+            // V: eight keys of four dims: lanes = 4 runs of keys x 8 words of a row, so that
+            // eight neighbouring stores fall into different banks
+            const uint32_t vf = smem_u32(smem + G::vf_off) + st * G::k16;
+            const bool edge = key0 + kTileKeys > every;
+#pragma unroll 1
+            for (int e = t; e < (kTileKeys / 8) * (D / 4); e += 128) {
+                const int q = (e & 3) | ((e >> 5) & 3) << 2, w = ((e >> 2) & 7) | (e >> 7) << 3;
+                const uint8_t* src = raw + G::k8 + (q >> 1) * (kAttnStep * D);
+                uint32_t x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] = *reinterpret_cast<const uint32_t*>(src + AttnTile<D>::at(8 * (q & 1) + i, 4 * w & ~7) + (4 * w & 4));
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int key = key0 + 8 * q + i;
+                        if (key >= most) x[i] = 0;  // beyond the last row's keys: whatever lies there
+                        const uint32_t n = nan_bytes(x[i]);
+                        if (n) {  // a NaN code reaches the rows that see its key, through nan_key
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (n >> (8 * k) & 1u) atomicMin(nan_key + 4 * w + k, key);
+                            x[i] &= ~n;
+                        }
+                    }
+                }
+                uint32_t y[4][4];  // [dim][pair of keys]
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const Half4 a = e4m3x4_f16(__byte_perm(x[2 * i], x[2 * i + 1], 0x5140)), d = e4m3x4_f16(__byte_perm(x[2 * i], x[2 * i + 1], 0x7362));
+                    y[0][i] = a.lo;
+                    y[1][i] = a.hi;
+                    y[2][i] = d.lo;
+                    y[3][i] = d.hi;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int dim = 4 * w + k;
+                    sts_v4(vf + (q >> 3) * (D * 128) + dim * 128 + (((q ^ dim) & 7) << 4), y[k][0], y[k][1], y[k][2], y[k][3]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(vfull + 8 * st);
+                mbar_arrive(empty8 + 8 * st);
+            }
+        }
+        if (!ok && lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace fp4q

@@ -11,6 +11,7 @@
 
 #include "../../include/fp4q.h"
 #include "fp4q_attn.cuh"
+#include "fp4q_attn_tile.cuh"
 #include "fp4q_fp8.cuh"
 #include "fp4q_fp8_gemm.cuh"
 #include "fp4q_host.cuh"
@@ -296,19 +297,27 @@ namespace {
 // where there are too few tiles to fill the GPU (by the lengths' bound, since
 // the lengths are on the device).
 struct AttnPlan {
+    bool tile;  // attn_tile_kernel
     int64_t row_tiles, splits, chunk, slot_rows;
     size_t ws_bytes;
 };
 
 constexpr int64_t kAttnMost = (int64_t)1 << 30;
+constexpr int64_t kAttnTileFrom = 64;
 
 fp4q_status attn_plan(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_heads, int64_t kv_heads, int64_t dim,
                       int sms, AttnPlan* out) {
     AttnPlan a{};
     // rows and keys are counted in 31 bits, with room for the last tile
     if (max_len > kAttnMost || max_q > kAttnMost / (q_heads / kv_heads)) return FP4Q_ERR_UNSUPPORTED;
-    a.row_tiles = spans(max_q * (q_heads / kv_heads), kAttnRows);
+    const int64_t rows = max_q * (q_heads / kv_heads);
+    a.tile = dim <= 128 && rows >= kAttnTileFrom;
+    a.row_tiles = spans(rows, a.tile ? kTileRows : kAttnRows);
     if (a.row_tiles >= kMaxDim / kv_heads || a.row_tiles * kv_heads >= kMaxDim / batch) return FP4Q_ERR_UNSUPPORTED;
+    if (a.tile) {
+        *out = a;
+        return FP4Q_OK;
+    }
     a.slot_rows = std::min<int64_t>(kAttnRows, max_q * (q_heads / kv_heads));
     const int64_t items = batch * kv_heads * a.row_tiles;
     const int64_t want = std::max<int64_t>(1, spans(3 * (int64_t)sms, items));
@@ -334,6 +343,18 @@ fp4q_status make_kv_map(CUtensorMap* map, const KvCacheView& c, const uint8_t* c
                      CU_TENSOR_MAP_INTERLEAVE_NONE, c.dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? FP4Q_OK : FP4Q_ERR_CUDA;
+}
+
+template <int D>
+fp4q_status launch_attn_tile(const AttnParams& p, const AttnPlan& a, cudaStream_t s) {
+    using G = AttnTileGeo<D>;
+    auto kern = attn_tile_kernel<D>;
+    static std::atomic<uint64_t> done{0};
+    fp4q_status st = ensure_smem(kern, G::smem, done);
+    if (st != FP4Q_OK) return st;
+    CUtensorMap map_k, map_v;
+    if ((st = make_kv_map(&map_k, p.c, p.c.k)) != FP4Q_OK || (st = make_kv_map(&map_v, p.c, p.c.v)) != FP4Q_OK) return st;
+    return launch(kern, (int)(p.batch * p.c.heads * a.row_tiles), G::threads, G::smem, s, map_k, map_v, p, (uint32_t)a.row_tiles);
 }
 
 template <int D>
@@ -414,6 +435,8 @@ FP4Q_API fp4q_status fp4q_attention_fp8(const void* q, int64_t ldq, int64_t toke
         if (!workspace || workspace_bytes < a.ws_bytes) return FP4Q_ERR_INVALID_ARG;
         if (!aligned(workspace, 16)) return FP4Q_ERR_ALIGNMENT;
     }
+    if (a.tile)
+        return p.c.dim == 64 ? launch_attn_tile<64>(p, a, (cudaStream_t)stream) : launch_attn_tile<128>(p, a, (cudaStream_t)stream);
     if (p.c.dim == 64) return launch_attn<64>(p, a, workspace, (cudaStream_t)stream);
     if (p.c.dim == 128) return launch_attn<128>(p, a, workspace, (cudaStream_t)stream);
     return launch_attn<256>(p, a, workspace, (cudaStream_t)stream);
