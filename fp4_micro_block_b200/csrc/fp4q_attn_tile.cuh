@@ -45,7 +45,7 @@ struct AttnTileGeo {
     static constexpr uint32_t s_col = 0, pv_col = 256, q_col = 384;
 };
 // Registers of the four warpgroups: 4 * 128 at launch.
-constexpr int kTileRegsRoles = 56, kTileRegsSoftmax = 136, kTileRegsOut = 208, kTileRegsConvert = 112;
+constexpr int kTileRegsRoles = 48, kTileRegsSoftmax = 152, kTileRegsOut = 200, kTileRegsConvert = 112;
 static_assert(kTileRegsRoles + kTileRegsSoftmax + kTileRegsOut + kTileRegsConvert == 4 * 128, "register split");
 
 // kind::f16, D fp32, A and B fp16, both K-major, M = 128.
@@ -95,6 +95,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A NaN code of V reaches the rows that see its key and no other: it counts as 0
+// in the product, and nan_key keeps the first such key of each of four dims.
+__device__ __noinline__ void attn_note_nans(int* nan_key, uint32_t bytes, int key) {
+    for (int e = 0; e < 4; ++e)
+        if (bytes >> (8 * e) & 1u) atomicMin(nan_key + e, key);
+}
 
 template <int D>
 __global__ void __launch_bounds__(512, 1)
@@ -278,53 +285,77 @@ __global__ void __launch_bounds__(512, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t sa = tmem + lanes + G::s_col + 128 * st;
+            // Two runs of 32 columns a turn, the next on its way under the arithmetic of
+            // this.  (The loops stay rolled: with all four roles unrolled the code did not
+            // fit the instruction caches, and a tile took three times as long.)
+            uint32_t xs[2][32];
             float top = -INFINITY;
+            tmem_start(sa, xs[0]);
+#pragma unroll 1
+            for (int c0 = 0; c0 < kTileKeys; c0 += 64) {
 #pragma unroll
-            for (int c = 0; c < kTileKeys / 32; ++c) {
-                uint32_t x[32];
-                tmem_start(sa + 32 * c, x);
-                tmem_wait(x);
-                if (edge) {
+                for (int cc = 0; cc < 2; ++cc) {
+                    uint32_t(&x)[32] = xs[cc];
+                    const int col = c0 + 32 * cc;
+                    tmem_wait(x);
+                    // (the last one starts the second pass)
+                    tmem_start(sa + ((col + 32) & (kTileKeys - 1)), xs[cc ^ 1]);
+                    if (edge) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = 32 * c + i < left ? x[i] : 0xff800000u;
-                }
+                        for (int i = 0; i < 32; ++i) x[i] = i < left - col ? x[i] : 0xff800000u;
+                    }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float mx = __uint_as_float(x[16 * h]);
+                    for (int h = 0; h < 2; ++h) {
+                        float mx[4];
 #pragma unroll
-                    for (int i = 1; i < 16; ++i) mx = fmaxf(mx, __uint_as_float(x[16 * h + i]));
-                    const float f = __shfl_sync(0xffffffffu, kv, 2 * c + h) * qs;
-                    top = fmaxf(top, mx * f + __shfl_sync(0xffffffffu, lv, 2 * c + h));  // (-inf * 0 is no number: skipped)
+                        for (int i = 0; i < 4; ++i)
+                            mx[i] = fmaxf(fmaxf(__uint_as_float(x[16 * h + i]), __uint_as_float(x[16 * h + 4 + i])),
+                                          fmaxf(__uint_as_float(x[16 * h + 8 + i]), __uint_as_float(x[16 * h + 12 + i])));
+                        const int run = col / 16 + h;
+                        const float f = __shfl_sync(0xffffffffu, kv, run) * qs;
+                        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f +
+                                             __shfl_sync(0xffffffffu, lv, run));  // (-inf * 0 is no number: skipped)
+                    }
                 }
             }
             const float mn = fmaxf(m, top), a = mn == -INFINITY ? 1.0f : exp2_approx(m - mn), base = mn == -INFINITY ? 0.0f : mn;
             m = mn;
             l *= a;
             alpha[(j & 3) * kTileRows + t] = a;
-            // P goes where S was: columns 16 c .. of S's are read by then
+            // P goes where S was: columns c .. of P overwrite columns of S that have been read
+            float sum[2] = {0.0f, 0.0f};
+            auto weights = [&](auto&& seen) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < kTileKeys; c0 += 64) {
 #pragma unroll
-            for (int c = 0; c < kTileKeys / 32; ++c) {
-                uint32_t x[32], w[16];
-                tmem_start(sa + 32 * c, x);
-                tmem_wait(x);
+                    for (int cc = 0; cc < 2; ++cc) {
+                        uint32_t(&x)[32] = xs[cc];
+                        const int col = c0 + 32 * cc;
+                        uint32_t w[16];
+                        tmem_wait(x);
+                        if (cc == 0 || c0 == 0) tmem_start(sa + col + 32, xs[cc ^ 1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float f = __shfl_sync(0xffffffffu, kv, 2 * c + h) * qs, wv = __shfl_sync(0xffffffffu, vv, 2 * c + h) * 0x1p14f;
-                    float sum = 0.0f;
+                        for (int h = 0; h < 2; ++h) {
+                            const int run = col / 16 + h;
+                            const float f = __shfl_sync(0xffffffffu, kv, run) * qs, wv = __shfl_sync(0xffffffffu, vv, run) * 0x1p14f;
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        float e0 = exp2_approx(fmaf(__uint_as_float(x[16 * h + i]), f, -base)), e1 = exp2_approx(fmaf(__uint_as_float(x[16 * h + i + 1]), f, -base));
-                        if (edge) {
-                            e0 = 32 * c + 16 * h + i < left ? e0 : 0.0f;
-                            e1 = 32 * c + 16 * h + i + 1 < left ? e1 : 0.0f;
+                            for (int i = 0; i < 16; i += 2) {
+                                const float e0 = seen(16 * h + i, left - col, exp2_approx(fmaf(__uint_as_float(x[16 * h + i]), f, -base)));
+                                const float e1 = seen(16 * h + i + 1, left - col, exp2_approx(fmaf(__uint_as_float(x[16 * h + i + 1]), f, -base)));
+                                sum[0] += e0;
+                                sum[1] += e1;
+                                w[8 * h + i / 2] = f16x2_pack(e0 * wv, e1 * wv);
+                            }
                         }
-                        sum += e0 + e1;
-                        w[8 * h + i / 2] = f16x2_pack(e0 * wv, e1 * wv);
+                        tmem_st16(sa + col / 2, w);
                     }
-                    l += sum;
                 }
-                tmem_st16(sa + 16 * c, w);
-            }
+            };
+            if (edge)
+                weights([](int i, int n, float e) { return i < n ? e : 0.0f; });
+            else
+                weights([](int, int, float e) { return e; });
+            l += sum[0] + sum[1];
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -387,6 +418,16 @@ __global__ void __launch_bounds__(512, 1)
         // ------------------------------------------------ conversion of the codes to fp16
         reg_dec<kTileRegsConvert>();
         const int t = tid & 127;
+        // K, eight codes of a key (one 16-byte piece of fp16) at a time: piece kc of keys
+        // kk, kk + kstep, ..; a row of a box or of the result is its key times the row's
+        // size further, at the same swizzle (kstep is a multiple of 8)
+        constexpr int kstep = 128 / (D / 8);
+        const int kc = t % (D / 8), kk = t / (D / 8);
+        const uint32_t ksrc = kk * D + (AttnTile<D>::at(kk & 15, 8 * kc) - (kk & 15) * D);
+        const uint32_t kdst = (kc >> 3) * (kTileKeys * 128) + kk * 128 + (((kc ^ kk) & 7) << 4);
+        // V, eight keys (run q) of four dims (word w0 + 8 i of a row): lanes are 4 runs x 8
+        // words, so that eight neighbouring stores fall into different banks
+        const int q = (t & 3) | (t >> 5) << 2, w0 = (t >> 2) & 7;
         bool ok = true;
         for (int j = 0; j < tiles; ++j) {
             const int st = j & 1, key0 = j * kTileKeys;
@@ -395,60 +436,55 @@ __global__ void __launch_bounds__(512, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint8_t* raw = smem + G::raw_off + st * 2 * G::k8;
-            const uint32_t kf = smem_u32(smem + G::kf_off) + st * G::k16;
-            // K: eight codes of a key (one 16-byte piece of fp16) at a time
-#pragma unroll 4
-            for (int e = t; e < kTileKeys * D / 8; e += 128) {
-                const int key = e / (D / 8), c = e % (D / 8);
-                const uint2 x = *reinterpret_cast<const uint2*>(raw + (key >> 4) * (kAttnStep * D) + AttnTile<D>::at(key & 15, 8 * c));
-                const Half4 a = e4m3x4_f16(x.x), d = e4m3x4_f16(x.y);
-                sts_v4(kf + (c >> 3) * (kTileKeys * 128) + key * 128 + (((c ^ key) & 7) << 4), a.lo, a.hi, d.lo, d.hi);
+            const uint32_t kf = smem_u32(smem + G::kf_off) + st * G::k16 + kdst;
+            constexpr int kn = kTileKeys / kstep;
+#pragma unroll
+            for (int i0 = 0; i0 < kn; i0 += 8) {
+                uint2 x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint2*>(raw + ksrc + (i0 + i) * kstep * D);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const Half4 a = e4m3x4_f16(x[i].x), d = e4m3x4_f16(x[i].y);
+                    sts_v4(kf + (i0 + i) * kstep * 128, a.lo, a.hi, d.lo, d.hi);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(kfull + 8 * st);
             ok = __all_sync(0xffffffffu, j < 2 || mbar_wait(vfree + 8 * st, ph ^ 1u));
             if (!ok) break;
-            // V: eight keys of four dims: lanes = 4 runs of keys x 8 words of a row, so that
-            // eight neighbouring stores fall into different banks
-            const uint32_t vf = smem_u32(smem + G::vf_off) + st * G::k16;
+            const uint32_t vf = smem_u32(smem + G::vf_off) + st * G::k16 + (q >> 3) * (D * 128) + 4 * w0 * 128;
+            const uint8_t* vsrc = raw + G::k8 + 8 * q * D + ((4 * w0) & 15);
             const bool edge = key0 + kTileKeys > every;
 #pragma unroll 1
-            for (int e = t; e < (kTileKeys / 8) * (D / 4); e += 128) {
-                const int q = (e & 3) | ((e >> 5) & 3) << 2, w = ((e >> 2) & 7) | (e >> 7) << 3;
-                const uint8_t* src = raw + G::k8 + (q >> 1) * (kAttnStep * D);
+            for (int i = 0; i < D / 32; ++i) {
                 uint32_t x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    x[i] = *reinterpret_cast<const uint32_t*>(src + AttnTile<D>::at(8 * (q & 1) + i, 4 * w & ~7) + (4 * w & 4));
+                for (int k = 0; k < 8; ++k)  // key 8 q + k: the row's 16-byte pieces are swizzled by its place in the box
+                    x[k] = *reinterpret_cast<const uint32_t*>(vsrc + AttnTile<D>::at(8 * (q & 1) + k, ((4 * w0) & 16) + 32 * i) - 8 * (q & 1) * D);
                 if (edge) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int key = key0 + 8 * q + i;
-                        if (key >= most) x[i] = 0;  // beyond the last row's keys: whatever lies there
-                        const uint32_t n = nan_bytes(x[i]);
-                        if (n) {  // a NaN code reaches the rows that see its key, through nan_key
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (n >> (8 * k) & 1u) atomicMin(nan_key + 4 * w + k, key);
-                            x[i] &= ~n;
-                        }
+                    for (int k = 0; k < 8; ++k) {
+                        const int key = key0 + 8 * q + k;
+                        if (key >= most) x[k] = 0;  // beyond the last row's keys: whatever lies there
+                        const uint32_t n = nan_bytes(x[k]);
+                        if (n) attn_note_nans(nan_key + 4 * w0 + 32 * i, n, key);
+                        x[k] &= ~n;
                     }
                 }
                 uint32_t y[4][4];  // [dim][pair of keys]
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const Half4 a = e4m3x4_f16(__byte_perm(x[2 * i], x[2 * i + 1], 0x5140)), d = e4m3x4_f16(__byte_perm(x[2 * i], x[2 * i + 1], 0x7362));
-                    y[0][i] = a.lo;
-                    y[1][i] = a.hi;
-                    y[2][i] = d.lo;
-                    y[3][i] = d.hi;
+                for (int k = 0; k < 4; ++k) {
+                    const Half4 a = e4m3x4_f16(__byte_perm(x[2 * k], x[2 * k + 1], 0x5140)), d = e4m3x4_f16(__byte_perm(x[2 * k], x[2 * k + 1], 0x7362));
+                    y[0][k] = a.lo;
+                    y[1][k] = a.hi;
+                    y[2][k] = d.lo;
+                    y[3][k] = d.hi;
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int dim = 4 * w + k;
-                    sts_v4(vf + (q >> 3) * (D * 128) + dim * 128 + (((q ^ dim) & 7) << 4), y[k][0], y[k][1], y[k][2], y[k][3]);
-                }
+                for (int k = 0; k < 4; ++k)
+                    sts_v4(vf + (32 * i + k) * 128 + (((q ^ (4 * w0 + k)) & 7) << 4), y[k][0], y[k][1], y[k][2], y[k][3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
