@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(512, 1)
             l *= a;
             alpha[(j & 3) * kTileRows + t] = a;
             // P goes where S was: columns c .. of P overwrite columns of S that have been read
-            float sum[2] = {0.0f, 0.0f};
+            uint64_t sum = 0;
+            const uint64_t nb = f2_both(-base);
             auto weights = [&](auto&& seen) {
 #pragma unroll 1
                 for (int c0 = 0; c0 < kTileKeys; c0 += 64) {
@@ -337,14 +338,15 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int run = col / 16 + h;
-                            const float f = __shfl_sync(0xffffffffu, kv, run) * qs, wv = __shfl_sync(0xffffffffu, vv, run) * 0x1p14f;
+                            const uint64_t f = f2_both(__shfl_sync(0xffffffffu, kv, run) * qs), wv = f2_both(__shfl_sync(0xffffffffu, vv, run) * 0x1p14f);
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                const float e0 = seen(16 * h + i, left - col, exp2_approx(fmaf(__uint_as_float(x[16 * h + i]), f, -base)));
-                                const float e1 = seen(16 * h + i + 1, left - col, exp2_approx(fmaf(__uint_as_float(x[16 * h + i + 1]), f, -base)));
-                                sum[0] += e0;
-                                sum[1] += e1;
-                                w[8 * h + i / 2] = f16x2_pack(e0 * wv, e1 * wv);
+                                const uint64_t z = f2_fma(f2_pack(x[16 * h + i], x[16 * h + i + 1]), f, nb);
+                                const uint64_t e = f2_pack(__float_as_uint(seen(16 * h + i, left - col, exp2_approx(f2_lo(z)))),
+                                                           __float_as_uint(seen(16 * h + i + 1, left - col, exp2_approx(f2_hi(z)))));
+                                sum = f2_add(sum, e);
+                                const uint64_t y = f2_mul(e, wv);
+                                w[8 * h + i / 2] = f16x2_pack(f2_lo(y), f2_hi(y));
                             }
                         }
                         tmem_st16(sa + col / 2, w);
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(512, 1)
                 weights([](int i, int n, float e) { return i < n ? e : 0.0f; });
             else
                 weights([](int, int, float e) { return e; });
-            l += sum[0] + sum[1];
+            l += f2_lo(sum) + f2_hi(sum);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(512, 1)
             const uint32_t vf = smem_u32(smem + G::vf_off) + st * G::k16 + (q >> 3) * (D * 128) + 4 * w0 * 128;
             const uint8_t* vsrc = raw + G::k8 + 8 * q * D + ((4 * w0) & 15);
             const bool edge = key0 + kTileKeys > every;
-#pragma unroll 1
+#pragma unroll 2
             for (int i = 0; i < D / 32; ++i) {
                 uint32_t x[8];
 #pragma unroll
