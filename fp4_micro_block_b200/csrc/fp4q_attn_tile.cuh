@@ -11,10 +11,13 @@
 // K-major operands).  Numerics as in fp4q_attn.cuh: the page scales of K and V
 // are applied to S and P, which are fp32 until P is rounded.
 //
-// Warpgroups: 0  warp 0 TMA, warp 1 MMA issue;
-//             1  softmax: thread = row;
-//             2  output: thread = row, O in registers, O = O alpha + P V per tile;
-//             3  conversion.
+// Warpgroups: 0     warp 0 TMA, warp 1 MMA issue;
+//             1, 2  softmax of the even and of the odd tiles: thread = row, each
+//                   with a maximum and a denominator of its own (one warp per SM
+//                   quarter leaves most issue slots empty);
+//             3     output: thread = row, O in registers; P V of a tile is added
+//                   under the larger of the two maxima;
+//             4     conversion.
 // Every wait is bounded; one that runs out sets g_device_error, and the role stops.
 #pragma once
 
@@ -27,15 +30,16 @@ constexpr int kTileRows = 128, kTileKeys = 128;
 
 template <int D>
 struct AttnTileGeo {
-    static constexpr int threads = 512;
+    static constexpr int threads = 640;
     static constexpr int k8 = kTileKeys * D;          // bytes of a tile's K (or V) codes
     static constexpr int k16 = 2 * kTileKeys * D;     // as fp16
     static constexpr int raw_off = 0;                 // two stages of K and V codes
     static constexpr int kf_off = raw_off + 4 * k8;   // two buffers of K, two of V^T
     static constexpr int vf_off = kf_off + 2 * k16;
-    static constexpr int alpha_off = vf_off + 2 * k16;              // [4][128]
-    static constexpr int ml_off = alpha_off + 4 * kTileRows * 4;    // [2][128]: maxima, denominators
-    static constexpr int nan_off = ml_off + 2 * kTileRows * 4;      // [D]: first key with a NaN in V's column
+    static constexpr int mref_off = vf_off + 2 * k16;               // [4][128]: the maximum each tile's P is under
+    static constexpr int ml_off = mref_off + 4 * kTileRows * 4;     // [2][2][128]: maxima, denominators
+    static constexpr int qs_off = ml_off + 4 * kTileRows * 4;       // [128]: the queries' scales
+    static constexpr int nan_off = qs_off + kTileRows * 4;      // [D]: first key with a NaN in V's column
     static constexpr int bar_off = nan_off + D * 4;
     static constexpr int num_bars = 21;
     static constexpr int slot_off = bar_off + 8 * num_bars;
@@ -44,9 +48,9 @@ struct AttnTileGeo {
     // tensor memory columns
     static constexpr uint32_t s_col = 0, pv_col = 256, q_col = 384;
 };
-// Registers of the four warpgroups: 4 * 128 at launch.
-constexpr int kTileRegsRoles = 48, kTileRegsSoftmax = 152, kTileRegsOut = 200, kTileRegsConvert = 112;
-static_assert(kTileRegsRoles + kTileRegsSoftmax + kTileRegsOut + kTileRegsConvert == 4 * 128, "register split");
+// Registers of the five warpgroups: 5 * 96 at launch.
+constexpr int kTileRegsRoles = 32, kTileRegsSoftmax = 96, kTileRegsOut = 168, kTileRegsConvert = 88;
+static_assert(kTileRegsRoles + 2 * kTileRegsSoftmax + kTileRegsOut + kTileRegsConvert == 5 * 96, "register split");
 
 // kind::f16, D fp32, A and B fp16, both K-major, M = 128.
 __host__ __device__ constexpr uint32_t f16_idesc(int n) {
@@ -60,7 +64,7 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t bde
         "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Starts the load of 32 consecutive fp32 columns of this thread's TMEM lane; the
+// Starts the load of 32 or 16 consecutive fp32 columns of this thread's TMEM lane; the
 // registers hold them after tmem_wait of the same array.
 __device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -86,6 +90,22 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
         :
         : "memory");
 }
+__device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
 // 16 words into this thread's TMEM lane; complete after tmem_wait_st.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -104,7 +124,7 @@ __device__ __noinline__ void attn_note_nans(int* nan_key, uint32_t bytes, int ke
 }
 
 template <int D>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(640, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const AttnParams p, const uint32_t row_tiles) {
     using G = AttnTileGeo<D>;
@@ -115,7 +135,8 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t full8 = bars, empty8 = bars + 16, kfull = bars + 32, kfree = bars + 48, vfull = bars + 64,
                    vfree = bars + 80, sfull = bars + 96, pfull = bars + 112, pvfull = bars + 128, pvfree = bars + 136,
                    qfull = bars + 144, lfull = bars + 152, done_bar = bars + 160;
-    float* alpha = reinterpret_cast<float*>(smem + G::alpha_off);
+    float* mref = reinterpret_cast<float*>(smem + G::mref_off);
+    float* q_scale = reinterpret_cast<float*>(smem + G::qs_off);
     float* ml = reinterpret_cast<float*>(smem + G::ml_off);
     int* nan_key = reinterpret_cast<int*>(smem + G::nan_off);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::slot_off);
@@ -135,11 +156,11 @@ __global__ void __launch_bounds__(512, 1)
         mbar_init(pvfull, 1);
         mbar_init(pvfree, 4);
         mbar_init(qfull, 4);
-        mbar_init(lfull, 4);
+        mbar_init(lfull, 8);
         mbar_init(done_bar, 1);
         fence_barrier_init();
     }
-    for (int i = tid; i < D; i += 512) nan_key[i] = 0x7fffffff;
+    for (int i = tid; i < D; i += 640) nan_key[i] = 0x7fffffff;
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
@@ -223,14 +244,13 @@ __global__ void __launch_bounds__(512, 1)
             tc_commit(done_bar);
             if (!mbar_wait(done_bar, 0)) atomicOr(&g_device_error, kErrWaitTimeout);
         }
-    } else if (wg == 1) {
+    } else if (wg <= 2) {
         // ------------------------------------------------ softmax: thread = row
-        reg_inc<kTileRegsSoftmax>();
+        const int odd = wg - 1;
         const int t = tid & 127, r = r0 + t;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's TMEM lanes
         const int lim = rows > 0 ? attn_limit(p, s, r) : 0;
-        float qs = 0.0f;
-        {
+        if (!odd) {
             // the row's query as fp16, scaled by a power of two to a maximum of 2^14, its sign that of the softmax scale
             const bool live = t < rows;
             const uint32_t rr = live ? r : 0, tok = rr / (uint32_t)p.group, h = hk * p.group + (rr - tok * p.group);
@@ -246,7 +266,7 @@ __global__ void __launch_bounds__(512, 1)
             int e = amax == 0.0f ? 0 : 14 + 127 - (int)(__float_as_uint(fmaxf(amax, 0x1p-126f)) >> 23);
             const int e1 = e / 2, e2 = e - e1;
             const float u1 = __int_as_float((127 + e1) << 23) * (p.scale_log2 < 0.0f ? -1.0f : 1.0f), u2 = __int_as_float((127 + e2) << 23);
-            qs = __int_as_float((127 - e1) << 23) * __int_as_float((127 - e2) << 23) * fabsf(p.scale_log2);
+            q_scale[t] = __int_as_float((127 - e1) << 23) * __int_as_float((127 - e2) << 23) * fabsf(p.scale_log2);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t w[16];
@@ -272,85 +292,73 @@ __global__ void __launch_bounds__(512, 1)
                 vn = __ldg(p.c.v_scale + at);
             }
         };
-        scales(0);
+        scales(odd);
         float m = -INFINITY, l = 0.0f;
-        bool ok = true;
-        for (int j = 0; j < tiles; ++j) {
+        bool ok = __all_sync(0xffffffffu, mbar_wait(qfull, 0));
+        const float qs = q_scale[t];
+        for (int j = odd; j < tiles && ok; j += 2) {
             const int st = j & 1;
             const float kv = kn, vv = vn, lv = log2f(fmaxf(vn, 0x1p-100f));
-            if (j + 1 < tiles) scales(j + 1);
+            if (j + 2 < tiles) scales(j + 2);
             const int left = lim - j * kTileKeys;  // keys of the tile that this row sees
             const bool edge = (j + 1) * kTileKeys > every;
             ok = __all_sync(0xffffffffu, mbar_wait(sfull + 8 * st, (uint32_t)((j >> 1) & 1)));
             if (!ok) break;
             tc_fence_after();
             const uint32_t sa = tmem + lanes + G::s_col + 128 * st;
-            // Two runs of 32 columns a turn, the next on its way under the arithmetic of
-            // this.  (The loops stay rolled: with all four roles unrolled the code did not
-            // fit the instruction caches, and a tile took three times as long.)
-            uint32_t xs[2][32];
+            // (The loops stay rolled: with all roles unrolled the code did not fit the
+            // instruction caches, and a tile took twice as long.)
             float top = -INFINITY;
-            tmem_start(sa, xs[0]);
 #pragma unroll 1
-            for (int c0 = 0; c0 < kTileKeys; c0 += 64) {
+            for (int col = 0; col < kTileKeys; col += 32) {
+                uint32_t x[32];
+                tmem_start(sa + col, x);
+                tmem_wait(x);
+                if (edge) {
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc) {
-                    uint32_t(&x)[32] = xs[cc];
-                    const int col = c0 + 32 * cc;
-                    tmem_wait(x);
-                    // (the last one starts the second pass)
-                    tmem_start(sa + ((col + 32) & (kTileKeys - 1)), xs[cc ^ 1]);
-                    if (edge) {
+                    for (int i = 0; i < 32; ++i) x[i] = i < left - col ? x[i] : 0xff800000u;
+                }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = i < left - col ? x[i] : 0xff800000u;
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    float mx[4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float mx[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mx[i] = fmaxf(fmaxf(__uint_as_float(x[16 * h + i]), __uint_as_float(x[16 * h + 4 + i])),
-                                          fmaxf(__uint_as_float(x[16 * h + 8 + i]), __uint_as_float(x[16 * h + 12 + i])));
-                        const int run = col / 16 + h;
-                        const float f = __shfl_sync(0xffffffffu, kv, run) * qs;
-                        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f +
-                                             __shfl_sync(0xffffffffu, lv, run));  // (-inf * 0 is no number: skipped)
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        mx[i] = fmaxf(fmaxf(__uint_as_float(x[16 * h + i]), __uint_as_float(x[16 * h + 4 + i])),
+                                      fmaxf(__uint_as_float(x[16 * h + 8 + i]), __uint_as_float(x[16 * h + 12 + i])));
+                    const int run = col / 16 + h;
+                    const float f = __shfl_sync(0xffffffffu, kv, run) * qs;
+                    top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f +
+                                         __shfl_sync(0xffffffffu, lv, run));  // (-inf * 0 is no number: skipped)
                 }
             }
             const float mn = fmaxf(m, top), a = mn == -INFINITY ? 1.0f : exp2_approx(m - mn), base = mn == -INFINITY ? 0.0f : mn;
             m = mn;
             l *= a;
-            alpha[(j & 3) * kTileRows + t] = a;
+            mref[(j & 3) * kTileRows + t] = mn;
             // P goes where S was: columns c .. of P overwrite columns of S that have been read
             uint64_t sum = 0;
             const uint64_t nb = f2_both(-base);
             auto weights = [&](auto&& seen) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < kTileKeys; c0 += 64) {
+                for (int col = 0; col < kTileKeys; col += 32) {
+                    uint32_t x[32], w[16];
+                    tmem_start(sa + col, x);
+                    tmem_wait(x);
 #pragma unroll
-                    for (int cc = 0; cc < 2; ++cc) {
-                        uint32_t(&x)[32] = xs[cc];
-                        const int col = c0 + 32 * cc;
-                        uint32_t w[16];
-                        tmem_wait(x);
-                        if (cc == 0 || c0 == 0) tmem_start(sa + col + 32, xs[cc ^ 1]);
+                    for (int h = 0; h < 2; ++h) {
+                        const int run = col / 16 + h;
+                        const uint64_t f = f2_both(__shfl_sync(0xffffffffu, kv, run) * qs), wv = f2_both(__shfl_sync(0xffffffffu, vv, run) * 0x1p14f);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int run = col / 16 + h;
-                            const uint64_t f = f2_both(__shfl_sync(0xffffffffu, kv, run) * qs), wv = f2_both(__shfl_sync(0xffffffffu, vv, run) * 0x1p14f);
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const uint64_t z = f2_fma(f2_pack(x[16 * h + i], x[16 * h + i + 1]), f, nb);
-                                const uint64_t e = f2_pack(__float_as_uint(seen(16 * h + i, left - col, exp2_approx(f2_lo(z)))),
-                                                           __float_as_uint(seen(16 * h + i + 1, left - col, exp2_approx(f2_hi(z)))));
-                                sum = f2_add(sum, e);
-                                const uint64_t y = f2_mul(e, wv);
-                                w[8 * h + i / 2] = f16x2_pack(f2_lo(y), f2_hi(y));
-                            }
+                        for (int i = 0; i < 16; i += 2) {
+                            const uint64_t z = f2_fma(f2_pack(x[16 * h + i], x[16 * h + i + 1]), f, nb);
+                            const uint64_t e = f2_pack(__float_as_uint(seen(16 * h + i, left - col, exp2_approx(f2_lo(z)))),
+                                                       __float_as_uint(seen(16 * h + i + 1, left - col, exp2_approx(f2_hi(z)))));
+                            sum = f2_add(sum, e);
+                            const uint64_t y = f2_mul(e, wv);
+                            w[8 * h + i / 2] = f16x2_pack(f2_lo(y), f2_hi(y));
                         }
-                        tmem_st16(sa + col / 2, w);
                     }
+                    tmem_st16(sa + col / 2, w);
                 }
             };
             if (edge)
@@ -364,11 +372,11 @@ __global__ void __launch_bounds__(512, 1)
             if (lane == 0) mbar_arrive(pfull + 8 * st);
         }
         if (!ok && lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
-        ml[t] = m;
-        ml[kTileRows + t] = l;
+        ml[2 * odd * kTileRows + t] = m;
+        ml[(2 * odd + 1) * kTileRows + t] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(lfull);
-    } else if (wg == 2) {
+    } else if (wg == 3) {
         // ------------------------------------------------ output: thread = row
         reg_inc<kTileRegsOut>();
         const int t = tid & 127, r = r0 + t;
@@ -376,19 +384,23 @@ __global__ void __launch_bounds__(512, 1)
         uint64_t o[D / 2];
 #pragma unroll
         for (int d = 0; d < D / 2; ++d) o[d] = 0;
+        float mo = -INFINITY;
         bool ok = true;
         for (int j = 0; j < tiles; ++j) {
             ok = __all_sync(0xffffffffu, mbar_wait(pvfull, (uint32_t)(j & 1)));
             if (!ok) break;
             tc_fence_after();
-            const uint64_t a = f2_both(alpha[(j & 3) * kTileRows + t]);
+            const float mj = mref[(j & 3) * kTileRows + t], mn = fmaxf(mo, mj);
+            // (-inf: nothing seen so far, or in this tile)
+            const uint64_t a = f2_both(mo == -INFINITY ? 1.0f : exp2_approx(mo - mn)), w = f2_both(mj == -INFINITY ? 1.0f : exp2_approx(mj - mn));
+            mo = mn;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t x[32];
-                tmem_start(tmem + lanes + G::pv_col + 32 * c, x);
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t x[16];
+                tmem_start(tmem + lanes + G::pv_col + 16 * c, x);
                 tmem_wait(x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[16 * c + i] = f2_fma(o[16 * c + i], a, f2_pack(x[2 * i], x[2 * i + 1]));
+                for (int i = 0; i < 8; ++i) o[8 * c + i] = f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), w, f2_mul(o[8 * c + i], a));
             }
             tc_fence_before();
             __syncwarp();
@@ -397,7 +409,13 @@ __global__ void __launch_bounds__(512, 1)
         ok = ok && __all_sync(0xffffffffu, mbar_wait(lfull, 0));
         if (!ok && lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
         if (t < rows) {
-            const float m = ml[t], l = ml[kTileRows + t], inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
+            float l = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float mk = ml[2 * k * kTileRows + t];
+                l = fmaf(ml[(2 * k + 1) * kTileRows + t], mk == -INFINITY ? 1.0f : exp2_approx(mk - mo), l);
+            }
+            const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
             const int lim = attn_limit(p, s, r);
             const uint32_t tok = (uint32_t)r / (uint32_t)p.group, h = hk * p.group + (r - tok * p.group);
             uint4* dst = reinterpret_cast<uint4*>(p.o + (s.first + tok) * p.ldo + (int64_t)h * D);
@@ -414,7 +432,7 @@ __global__ void __launch_bounds__(512, 1)
                     if (nan_key[8 * c + i] < lim) v[i] = __int_as_float(0x7fffffff);
                 dst[c] = make_uint4(bf16x2_pack(v[0], v[1]), bf16x2_pack(v[2], v[3]), bf16x2_pack(v[4], v[5]), bf16x2_pack(v[6], v[7]));
             }
-            if (p.lse) p.lse[(s.first + tok) * p.q_heads + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (p.lse) p.lse[(s.first + tok) * p.q_heads + h] = l == 0.0f ? -INFINITY : (mo + log2f(l)) * kLn2;
         }
     } else {
         // ------------------------------------------------ conversion of the codes to fp16
