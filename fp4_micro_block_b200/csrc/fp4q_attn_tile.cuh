@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(640, 1)
                 __syncwarp();
             }
         } else if (warp == 1 && lane == 0 && tiles > 0) {
-            // -------------------------------------------- MMA: S of tile j + 1 goes before P V of tile j
+            // -------------------------------------------- MMA: S runs two tiles ahead of P V
             bool ok = mbar_wait(qfull, 0);
             auto issue_s = [&](int j) {
                 const int st = j & 1;
@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(640, 1)
                 tc_commit(sfull + 8 * st);
             };
             issue_s(0);
+            if (tiles > 1) issue_s(1);
             for (int j = 0; j < tiles && ok; ++j) {
-                if (j + 1 < tiles) issue_s(j + 1);
                 const int st = j & 1;
                 ok = ok && mbar_wait(vfull + 8 * st, (uint32_t)((j >> 1) & 1)) &&
                      mbar_wait(pfull + 8 * st, (uint32_t)((j >> 1) & 1)) && (j == 0 || mbar_wait(pvfree, (uint32_t)((j - 1) & 1)));
@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(640, 1)
                                 sw128_desc(v + (i >> 2) * (D * 128) + (i & 3) * 32), f16_idesc(D), i > 0);
                 tc_commit(vfree + 8 * st);
                 tc_commit(pvfull);
+                if (j + 2 < tiles) issue_s(j + 2);  // over P of tile j, in order behind its product
             }
             if (!ok) atomicOr(&g_device_error, kErrWaitTimeout);
             // all MMAs complete before TMEM is freed
