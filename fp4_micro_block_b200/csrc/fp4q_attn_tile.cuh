@@ -56,6 +56,17 @@ static_assert(kTileRegsRoles + 2 * kTileRegsSoftmax + kTileRegsOut + kTileRegsCo
 __host__ __device__ constexpr uint32_t f16_idesc(int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
+// sw128_desc in two parts: the low word, to which offsets / 16 are added, and the rest.
+__device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t saddr) { return (uint32_t)sw128_desc(saddr); }
+__device__ __forceinline__ uint64_t sw128_desc_of(uint32_t lo) {
+    return (uint64_t)lo | ((uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32);
+}
+// One lane of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
 // D[tmem] (+)= A[tmem] * B[smem]^T, K = 16.
 __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -207,43 +218,55 @@ __global__ void __launch_bounds__(640, 1)
                 }
                 __syncwarp();
             }
-        } else if (warp == 1 && lane == 0 && tiles > 0) {
+        } else if (warp == 1 && tiles > 0) {
             // -------------------------------------------- MMA: S runs two tiles ahead of P V
-            bool ok = mbar_wait(qfull, 0);
+            // The whole warp goes through the loop, so that addresses stay in uniform
+            // registers, and one lane issues.
+            const bool one = elect_one();
+            const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t kd = sw128_desc_lo(smem_u32(smem + G::kf_off)), vd = sw128_desc_lo(smem_u32(smem + G::vf_off));
+            bool ok = __all_sync(0xffffffffu, mbar_wait(qfull, 0));
             auto issue_s = [&](int j) {
                 const int st = j & 1;
-                ok = ok && mbar_wait(kfull + 8 * st, (uint32_t)((j >> 1) & 1));
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(kfull + 8 * st, (uint32_t)((j >> 1) & 1)));
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t k = smem_u32(smem + G::kf_off) + st * G::k16;
+                const uint32_t k = kd + st * (G::k16 >> 4);
+                if (one) {
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    umma_f16_ts(tmem + G::s_col + 128 * st, tmem + G::q_col + 8 * i,
-                                sw128_desc(k + (i >> 2) * (kTileKeys * 128) + (i & 3) * 32), f16_idesc(kTileKeys), i > 0);
-                tc_commit(kfree + 8 * st);
-                tc_commit(sfull + 8 * st);
+                    for (int i = 0; i < D / 16; ++i)
+                        umma_f16_ts(t0 + G::s_col + 128 * st, t0 + G::q_col + 8 * i,
+                                    sw128_desc_of(k + (((i >> 2) * (kTileKeys * 128) + (i & 3) * 32) >> 4)), f16_idesc(kTileKeys), i > 0);
+                    tc_commit(kfree + 8 * st);
+                    tc_commit(sfull + 8 * st);
+                }
+                __syncwarp();
             };
             issue_s(0);
             if (tiles > 1) issue_s(1);
             for (int j = 0; j < tiles && ok; ++j) {
                 const int st = j & 1;
-                ok = ok && mbar_wait(vfull + 8 * st, (uint32_t)((j >> 1) & 1)) &&
-                     mbar_wait(pfull + 8 * st, (uint32_t)((j >> 1) & 1)) && (j == 0 || mbar_wait(pvfree, (uint32_t)((j - 1) & 1)));
+                ok = mbar_wait(vfull + 8 * st, (uint32_t)((j >> 1) & 1)) && mbar_wait(pfull + 8 * st, (uint32_t)((j >> 1) & 1)) &&
+                     (j == 0 || mbar_wait(pvfree, (uint32_t)((j - 1) & 1)));
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t v = smem_u32(smem + G::vf_off) + st * G::k16;
+                const uint32_t v = vd + st * (G::k16 >> 4);
+                if (one) {
 #pragma unroll
-                for (int i = 0; i < kTileKeys / 16; ++i)
-                    umma_f16_ts(tmem + G::pv_col, tmem + G::s_col + 128 * st + 8 * i,
-                                sw128_desc(v + (i >> 2) * (D * 128) + (i & 3) * 32), f16_idesc(D), i > 0);
-                tc_commit(vfree + 8 * st);
-                tc_commit(pvfull);
+                    for (int i = 0; i < kTileKeys / 16; ++i)
+                        umma_f16_ts(t0 + G::pv_col, t0 + G::s_col + 128 * st + 8 * i,
+                                    sw128_desc_of(v + (((i >> 2) * (D * 128) + (i & 3) * 32) >> 4)), f16_idesc(D), i > 0);
+                    tc_commit(vfree + 8 * st);
+                    tc_commit(pvfull);
+                }
+                __syncwarp();
                 if (j + 2 < tiles) issue_s(j + 2);  // over P of tile j, in order behind its product
             }
-            if (!ok) atomicOr(&g_device_error, kErrWaitTimeout);
+            if (!ok && one) atomicOr(&g_device_error, kErrWaitTimeout);
             // all MMAs complete before TMEM is freed
-            tc_commit(done_bar);
-            if (!mbar_wait(done_bar, 0)) atomicOr(&g_device_error, kErrWaitTimeout);
+            if (one) tc_commit(done_bar);
+            if (!mbar_wait(done_bar, 0) && one) atomicOr(&g_device_error, kErrWaitTimeout);
         }
     } else if (wg <= 2) {
         // ------------------------------------------------ softmax: thread = row
