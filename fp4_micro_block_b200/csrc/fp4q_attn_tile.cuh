@@ -56,17 +56,6 @@ static_assert(kTileRegsRoles + 2 * kTileRegsSoftmax + kTileRegsOut + kTileRegsCo
 __host__ __device__ constexpr uint32_t f16_idesc(int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-// sw128_desc in two parts: the low word, to which offsets / 16 are added, and the rest.
-__device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t saddr) { return (uint32_t)sw128_desc(saddr); }
-__device__ __forceinline__ uint64_t sw128_desc_of(uint32_t lo) {
-    return (uint64_t)lo | ((uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32);
-}
-// One lane of the (converged) warp, the same one each time.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
-    return r != 0;
-}
 // D[tmem] (+)= A[tmem] * B[smem]^T, K = 16.
 __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(

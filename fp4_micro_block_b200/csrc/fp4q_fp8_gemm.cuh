@@ -52,6 +52,17 @@ __host__ __device__ constexpr uint32_t f8_idesc(int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kF8Lanes >> 4) << 24);
 }
 
+// sw128_desc in two parts: the low word, to which offsets / 16 are added, and the rest.
+__device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t saddr) { return (uint32_t)sw128_desc(saddr); }
+__device__ __forceinline__ uint64_t sw128_desc_of(uint32_t lo) {
+    return (uint64_t)lo | ((uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32);
+}
+// One lane of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
 // D[tmem] (+)= A * B^T, E4M3 operands, M = 128, K = 32.
 __device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accumulate) {
@@ -258,36 +269,40 @@ __global__ void __launch_bounds__(F8Geo<NT>::threads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            bool ok = true;
-            const int64_t total = n_my * kbs;
-            int s = 0;
-            uint32_t ph = 0;
-            for (int64_t g = 0; g < total; ++g) {
-                const int buf = (int)(g & 1);
-                if (!mbar_wait(full0 + 8 * s, ph) ||
-                    (g >= 2 && !mbar_wait(acce + 8 * buf, (uint32_t)(((g >> 1) - 1) & 1)))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + s * G::stage_bytes);
+        // The whole warp goes through the loop, so that addresses stay in uniform
+        // registers, and one lane issues.
+        const bool one = elect_one();
+        const uint32_t t0 = __shfl_sync(0xffffffffu, tmem_base, 0);
+        const uint32_t ring = sw128_desc_lo(smem_u32(smem));
+        bool ok = true;
+        const int64_t total = n_my * kbs;
+        int s = 0;
+        uint32_t ph = 0;
+        for (int64_t g = 0; g < total; ++g) {
+            const int buf = (int)(g & 1);
+            ok = mbar_wait(full0 + 8 * s, ph) && (g < 2 || mbar_wait(acce + 8 * buf, (uint32_t)(((g >> 1) - 1) & 1)));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t st = ring + s * (G::stage_bytes >> 4);
+            if (one) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    umma_f8(tmem_base + NT * buf, sw128_desc(st + 32 * j), sw128_desc(st + kF8LaneBytes + 32 * j),
+                    umma_f8(t0 + NT * buf, sw128_desc_of(st + 2 * j), sw128_desc_of(st + (kF8LaneBytes >> 4) + 2 * j),
                             f8_idesc(NT), j > 0 ? 1u : 0u);
                 tc_commit(empty0 + 8 * s);
                 tc_commit(accf + 8 * buf);
-                if (++s == S) {
-                    s = 0;
-                    ph ^= 1;
-                }
             }
-            if (!ok) atomicOr(&g_device_error, kErrWaitTimeout);
-            // all MMAs of this CTA complete before TMEM is freed
-            tc_commit(done_bar);
-            if (!mbar_wait(done_bar, 0)) atomicOr(&g_device_error, kErrWaitTimeout);
+            __syncwarp();
+            if (++s == S) {
+                s = 0;
+                ph ^= 1;
+            }
         }
+        if (!ok && one) atomicOr(&g_device_error, kErrWaitTimeout);
+        // all MMAs of this CTA complete before TMEM is freed
+        if (one) tc_commit(done_bar);
+        if (!mbar_wait(done_bar, 0) && one) atomicOr(&g_device_error, kErrWaitTimeout);
     } else if (epi >= 0) {
         // ------------------------------------------------ scale, accumulate, store
         if constexpr (G::wide) reg_inc<kF8RegsEpilogue>();
