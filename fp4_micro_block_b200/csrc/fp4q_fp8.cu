@@ -99,53 +99,94 @@ struct Fp8Operand {
     int tile;
 };
 
-// fp8_gemm_kernel<NT, VEC> with l's rows as lanes and c's as columns (NT = 256:
-// l = A; else l = B, its K blocks split over up to kF8MaxSplit CTAs while SMs
-// are free).
-template <int NT, bool VEC>
-fp4q_status launch_f8(const Fp8Operand& l, const Fp8Operand& c, int64_t K, Fp8GemmParams p, int sms, cudaStream_t s) {
-    using G = F8Geo<NT>;
-    auto kern = fp8_gemm_kernel<NT, VEC>;
-    static std::atomic<uint64_t> done{0};
-    fp4q_status st = ensure_smem(kern, G::smem, done);
-    if (st != FP4Q_OK) return st;
+template <typename... KArgs, typename... Args>
+fp4q_status launch_cluster(void (*kern)(KArgs...), int64_t grid, int cluster, int threads, int smem, cudaStream_t s,
+                           Args&&... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess ? FP4Q_OK : FP4Q_ERR_CUDA;
+}
+
+void f8_operands(Fp8GemmParams& p, const Fp8Operand& l, const Fp8Operand& c, int64_t lane_rows, int64_t col_rows) {
     p.RL = l.rows;
     p.RC = c.rows;
-    p.n_lt = spans(l.rows, kF8Lanes);
-    p.n_tiles = p.n_lt * spans(c.rows, NT);
-    if (p.n_tiles >= kMaxDim / kF8MaxSplit) return FP4Q_ERR_UNSUPPORTED;
+    p.n_lt = spans(l.rows, lane_rows);
+    p.n_tiles = p.n_lt * spans(c.rows, col_rows);
     p.sl = l.scales;
     p.ldsl = l.lds;
     p.l_tile = l.tile;
     p.sc = c.scales;
     p.ldsc = c.lds;
-    CUtensorMap map_l, map_c, map_d;
-    if ((st = make_f8_map(&map_l, l.codes, l.rows, K, l.ld, kF8Lanes)) != FP4Q_OK) return st;
-    if ((st = make_f8_map(&map_c, c.codes, c.rows, K, c.ld, NT)) != FP4Q_OK) return st;
-    map_d = map_l;  // a placeholder where no TMA store is made
-    int64_t grid;
-    if constexpr (G::wide) {
-        p.tma_store = p.ldd * (p.out_bf16 ? 2 : 4) % 16 == 0;
-        if (p.tma_store && (st = make_f8_out_map(&map_d, p.d, l.rows, c.rows, p.ldd, p.out_bf16)) != FP4Q_OK) return st;
-        grid = std::min<int64_t>(p.n_tiles, sms);
-    } else {
-        p.split = (int32_t)std::max<int64_t>(1, std::min<int64_t>({(int64_t)kF8MaxSplit, (int64_t)p.n_kb, sms / p.n_tiles}));
-        grid = p.n_tiles * p.split;
-    }
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.split;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)G::threads);
-    cfg.dynamicSmemBytes = (size_t)G::smem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, map_l, map_c, map_d, p) == cudaSuccess ? FP4Q_OK : FP4Q_ERR_CUDA;
+}
+
+// CTAs that share a narrow tile's K blocks.
+int64_t f8_split(int64_t tiles, int64_t n_kb, int sms) {
+    return std::max<int64_t>(1, std::min<int64_t>({(int64_t)kF8MaxSplit, n_kb, sms / tiles}));
+}
+
+// Whether the wide kernel is the faster one, by what both took on one B200: per
+// wave and K block 0.55 us with tile scales of B, 0.80 with row scales (narrow,
+// 128 columns: 0.62), 4 us besides (narrow: 4, and 4 more for a split's join).
+// Measured for N = K = 4096, tile scales, in us (wide / narrow): M = 100 20.6 /
+// 11.3, 256 20.9 / 19.0, 512 21.3 / 23.2, 800 21.9 / 44.9; 300 x 1000 x 513
+// 7.3 / 8.1; 1000 x 1024 x 2000 13.6 / 14.9; 200 x 16384 x 4096 23.2 / 45.4.
+bool f8_take_wide(int64_t M, int64_t N, int64_t n_kb, bool tile, int sms) {
+    if (M <= 64) return false;  // a wide tile would waste more than half of its lanes
+    const int64_t wide = spans(spans(M, kF8Lanes) * spans(N, F8Wide::n), sms) * n_kb * (tile ? 55 : 80) + 400;
+    const int64_t tiles = spans(M, 128) * spans(N, kF8Lanes), split = f8_split(tiles, n_kb, sms);
+    const int64_t narrow = spans(tiles * split, sms) * spans(n_kb, split) * 62 + (split > 1 ? 800 : 400);
+    return wide < narrow;
+}
+
+// A's rows as columns, B's as lanes; the K blocks of a tile are split over up to
+// kF8MaxSplit CTAs while SMs are free.
+template <int NT>
+fp4q_status launch_f8_narrow(const Fp8Operand& a, const Fp8Operand& b, int64_t K, Fp8GemmParams p, int sms,
+                             cudaStream_t s) {
+    using G = F8Narrow<NT>;
+    auto kern = fp8_gemm_narrow_kernel<NT>;
+    static std::atomic<uint64_t> done{0};
+    fp4q_status st = ensure_smem(kern, G::smem, done);
+    if (st != FP4Q_OK) return st;
+    f8_operands(p, b, a, kF8Lanes, NT);
+    if (p.n_tiles >= kMaxDim / kF8MaxSplit) return FP4Q_ERR_UNSUPPORTED;
+    CUtensorMap map_l, map_c;
+    if ((st = make_f8_map(&map_l, b.codes, b.rows, K, b.ld, kF8Lanes)) != FP4Q_OK) return st;
+    if ((st = make_f8_map(&map_c, a.codes, a.rows, K, a.ld, NT)) != FP4Q_OK) return st;
+    p.split = (int32_t)f8_split(p.n_tiles, p.n_kb, sms);
+    return launch_cluster(kern, p.n_tiles * p.split, p.split, G::threads, G::smem, s, map_l, map_c, p);
+}
+
+// 128 x 256 tiles, persistent.
+template <bool VEC>
+fp4q_status launch_f8_wide(const Fp8Operand& a, const Fp8Operand& b, int64_t K, Fp8GemmParams p, int sms,
+                           cudaStream_t s) {
+    auto kern = fp8_gemm_wide_kernel<VEC>;
+    static std::atomic<uint64_t> done{0};
+    fp4q_status st = ensure_smem(kern, F8Wide::smem, done);
+    if (st != FP4Q_OK) return st;
+    f8_operands(p, a, b, kF8Lanes, F8Wide::n);
+    CUtensorMap map_a, map_b, map_d;
+    if ((st = make_f8_map(&map_a, a.codes, a.rows, K, a.ld, kF8Lanes)) != FP4Q_OK) return st;
+    if ((st = make_f8_map(&map_b, b.codes, b.rows, K, b.ld, F8Wide::n)) != FP4Q_OK) return st;
+    map_d = map_a;  // a placeholder where no TMA store is made
+    // the TMA writes whole 16-byte pieces: a row of D has to end with one
+    const int64_t es = p.out_bf16 ? 2 : 4;
+    p.tma_store = p.ldd * es % 16 == 0 && b.rows * es % 16 == 0;
+    if (p.tma_store && (st = make_f8_out_map(&map_d, p.d, a.rows, b.rows, p.ldd, p.out_bf16)) != FP4Q_OK) return st;
+    const int grid = (int)std::min<int64_t>(p.n_tiles, sms);
+    return launch(kern, grid, F8Wide::threads, F8Wide::smem, s, map_a, map_b, map_d, p);
 }
 
 fp4q_status check_cache(const fp4q_kv_cache* c, KvCacheView* v) {
@@ -245,17 +286,14 @@ FP4Q_API fp4q_status fp4q_gemm_fp8(const uint8_t* a_codes, int64_t lda, const fl
     p.ldd = ldd;
     p.out_bf16 = d_bf16;
     p.split = 1;
-    // The wide kernel has a tile for at least half of the SMs, or A's rows fill
-    // no narrow tile's columns.
-    const int64_t wide_tiles = spans(M, kF8Lanes) * spans(N, 256);
-    if (M > 128 && 2 * wide_tiles > sms) {
-        if (b.tile) return launch_f8<256, false>(a, b, K, p, sms, (cudaStream_t)stream);
-        return launch_f8<256, true>(a, b, K, p, sms, (cudaStream_t)stream);
+    if (f8_take_wide(M, N, p.n_kb, b.tile != 0, sms)) {
+        if (b.tile) return launch_f8_wide<false>(a, b, K, p, sms, (cudaStream_t)stream);
+        return launch_f8_wide<true>(a, b, K, p, sms, (cudaStream_t)stream);
     }
-    if (M <= 16) return launch_f8<16, true>(b, a, K, p, sms, (cudaStream_t)stream);
-    if (M <= 32) return launch_f8<32, true>(b, a, K, p, sms, (cudaStream_t)stream);
-    if (M <= 64) return launch_f8<64, true>(b, a, K, p, sms, (cudaStream_t)stream);
-    return launch_f8<128, true>(b, a, K, p, sms, (cudaStream_t)stream);
+    if (M <= 16) return launch_f8_narrow<16>(a, b, K, p, sms, (cudaStream_t)stream);
+    if (M <= 32) return launch_f8_narrow<32>(a, b, K, p, sms, (cudaStream_t)stream);
+    if (M <= 64) return launch_f8_narrow<64>(a, b, K, p, sms, (cudaStream_t)stream);
+    return launch_f8_narrow<128>(a, b, K, p, sms, (cudaStream_t)stream);
 }
 
 FP4Q_API fp4q_status fp4q_kv_append_fp8(const void* k, int64_t ldk, const void* v, int64_t ldv, int64_t tokens,

@@ -38,11 +38,11 @@ struct Fp8GemmParams {
     int64_t n_lt, n_tiles;   // lane tiles; tiles (lane tile fastest)
     const float *sl, *sc;    // scales [n_kb, ld]
     int64_t ldsl, ldsc;
-    int32_t l_tile;          // the lane operand's scales are per 128 x 128 tile
+    int32_t l_tile;          // narrow kernel: B's scales are per 128 x 128 tile
     void* d;
     int64_t ldd;
     int32_t out_bf16;
-    int32_t tma_store;       // wide kernel: D's rows are 16 bytes apart in step
+    int32_t tma_store;       // wide kernel: D's rows begin and end on 16 bytes
     int32_t split;           // narrow kernel: CTAs of the cluster that share a tile's K blocks
 };
 
@@ -109,41 +109,6 @@ __device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
     return v;
 }
 
-// The wide kernel's register split: 384 threads start with 168 each; the first
-// warpgroup gives up 96 so that the two epilogue ones, which hold 128 sums per
-// thread, have 216 (72 + 2 * 216 = 3 * 168).
-constexpr int kF8RegsRoles = 72, kF8RegsEpilogue = 216;
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-template <int NT>
-struct F8Geo {
-    static constexpr bool wide = NT == 256;
-    static constexpr int groups = wide ? 2 : 1;          // epilogue groups of four warps
-    static constexpr int cols = NT / groups;             // accumulator columns of a thread
-    static constexpr int first_epi = wide ? 4 : 2;       // first epilogue warp (wide: whole warpgroups, see kF8Regs)
-    static constexpr int threads = 32 * first_epi + 128 * groups;
-    static constexpr int stage_bytes = kF8LaneBytes + NT * kFp8Block;
-    static constexpr int stages = wide ? 4 : (192 * 1024) / stage_bytes;
-    static constexpr int ring = stages * stage_bytes;
-    static constexpr int stg_off = ring;                 // wide: 4 KiB of output staging per epilogue warp
-    static constexpr int sc_off = stg_off + (wide ? 8 * 4096 : 0);  // column scales, two buffers per group
-    static constexpr int bar_off = sc_off + groups * 2 * cols * 4;
-    static constexpr int num_bars = 2 * stages + 5;
-    static constexpr int slot_off = bar_off + num_bars * 8;
-    static constexpr int smem = 896 + slot_off + 16;     // the base is 128-byte aligned, the ring 1024
-    static constexpr uint32_t tmem_cols = 2 * NT;        // two buffers
-    static_assert(stage_bytes % 1024 == 0, "stages keep the 1024-byte alignment of the swizzle");
-    static_assert(smem <= 227 * 1024, "shared memory");
-    static_assert(wide || ring >= cols * kF8Lanes * 4, "the ring holds the partial sums of the split");
-};
-
 // One element of D.
 __device__ __forceinline__ void f8_store(const Fp8GemmParams& p, int64_t m, int64_t n, float v) {
     if (p.out_bf16)
@@ -180,14 +145,33 @@ __device__ __forceinline__ void f8_accumulate(uint32_t taddr, float f, const flo
     }
 }
 
-// VEC: the column operand's scales are per row (the narrow kernel's always are).
-template <int NT, bool VEC>
-__global__ void __launch_bounds__(F8Geo<NT>::threads, 1)
-    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_l, const __grid_constant__ CUtensorMap map_c,
-                    const __grid_constant__ CUtensorMap map_d, const Fp8GemmParams p) {
-    using G = F8Geo<NT>;
+// ------------------------------------------------------------------ narrow kernel
+
+template <int NT>
+struct F8Narrow {
+    static constexpr int groups = NT >= 64 ? 2 : 1;      // epilogue groups of four warps
+    static constexpr int cols = NT / groups;             // accumulator columns of a thread
+    static constexpr int threads = 64 + 128 * groups;
+    static constexpr int stage_bytes = kF8LaneBytes + NT * kFp8Block;
+    static constexpr int stages = (192 * 1024) / stage_bytes;
+    static constexpr int ring = stages * stage_bytes;
+    static constexpr int sc_off = ring;                  // column scales, two buffers
+    static constexpr int bar_off = sc_off + 2 * NT * 4;
+    static constexpr int num_bars = 2 * stages + 5;
+    static constexpr int slot_off = bar_off + num_bars * 8;
+    static constexpr int smem = 1024 + slot_off + 16;
+    static constexpr uint32_t tmem_cols = 2 * NT;        // two buffers
+    static_assert(stage_bytes % 1024 == 0, "stages keep the 1024-byte alignment of the swizzle");
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static_assert(ring >= NT * kF8Lanes * 4, "the ring holds the partial sums of the split");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(F8Narrow<NT>::threads, 1)
+    fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_l, const __grid_constant__ CUtensorMap map_c,
+                           const Fp8GemmParams p) {
+    using G = F8Narrow<NT>;
     constexpr int S = G::stages, C = G::cols;
-    static_assert(VEC || G::wide, "the narrow kernel's columns are rows of A");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = align_shared<1024>(smem_raw);
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -220,12 +204,240 @@ __global__ void __launch_bounds__(F8Geo<NT>::threads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    // this CTA's tiles (the narrow kernel has one) and K blocks
-    const int64_t unit = G::wide ? (int64_t)blockIdx.x : (int64_t)blockIdx.x / p.split;
-    const int64_t step = G::wide ? (int64_t)gridDim.x : p.n_tiles;
-    const uint32_t rank = G::wide ? 0u : cluster_rank();
-    const int kb0 = G::wide ? 0 : (int)((int64_t)p.n_kb * rank / p.split);
-    const int kbs = (G::wide ? p.n_kb : (int)((int64_t)p.n_kb * (rank + 1) / p.split)) - kb0;
+    // this CTA's tile and its share of the K blocks
+    const int64_t tile = blockIdx.x / p.split;
+    const int rank = (int)(blockIdx.x - tile * p.split);
+    const int64_t lt = tile % p.n_lt, ct = tile / p.n_lt;
+    const int kb0 = (int)((int64_t)p.n_kb * rank / p.split);
+    const int kbs = (int)((int64_t)p.n_kb * (rank + 1) / p.split) - kb0;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int g = 0, s = 0;
+            uint32_t ph = 1;
+            for (; g < kbs; ++g) {
+                if (g >= S && !mbar_wait(empty0 + 8 * s, ph)) {
+                    atomicOr(&g_device_error, kErrWaitTimeout);
+                    break;
+                }
+                uint8_t* st = smem + s * G::stage_bytes;
+                const uint32_t bar = full0 + 8 * s;
+                mbar_arrive_expect_tx(bar, G::stage_bytes);
+                tma_load_2d(smem_u32(st), &map_l, (kb0 + g) * kFp8Block, (int32_t)(lt * kF8Lanes), bar);
+                tma_load_2d(smem_u32(st + kF8LaneBytes), &map_c, (kb0 + g) * kFp8Block, (int32_t)(ct * NT), bar);
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            // every issued copy lands before the CTA may exit
+            for (int k = (g > S ? g - S : 0); k < g; ++k)
+                (void)mbar_wait(full0 + 8 * (k % S), (uint32_t)((k / S) & 1));
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        // The whole warp goes through the loop, so that addresses stay in uniform
+        // registers, and one lane issues.
+        const bool one = elect_one();
+        const uint32_t t0 = __shfl_sync(0xffffffffu, tmem_base, 0);
+        const uint32_t ring = sw128_desc_lo(smem_u32(smem));
+        bool ok = true;
+        int s = 0;
+        uint32_t ph = 0;
+        for (int g = 0; g < kbs; ++g) {
+            const int buf = (int)(g & 1);
+            ok = mbar_wait(full0 + 8 * s, ph) && (g < 2 || mbar_wait(acce + 8 * buf, (uint32_t)(((g >> 1) - 1) & 1)));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t st = ring + s * (G::stage_bytes >> 4);
+            if (one) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    umma_f8(t0 + NT * buf, sw128_desc_of(st + 2 * j), sw128_desc_of(st + (kF8LaneBytes >> 4) + 2 * j),
+                            f8_idesc(NT), j > 0 ? 1u : 0u);
+                tc_commit(empty0 + 8 * s);
+                tc_commit(accf + 8 * buf);
+            }
+            __syncwarp();
+            if (++s == S) {
+                s = 0;
+                ph ^= 1;
+            }
+        }
+        if (!ok && one) atomicOr(&g_device_error, kErrWaitTimeout);
+        // all MMAs of this CTA complete before TMEM is freed
+        if (one) tc_commit(done_bar);
+        if (!mbar_wait(done_bar, 0) && one) atomicOr(&g_device_error, kErrWaitTimeout);
+    } else {
+        // ------------------------------------------------ scale, accumulate, store
+        const uint32_t quarter = warp & 3;         // the TMEM lanes this warp may read
+        const int grp = (int)(warp - 2) >> 2;
+        const int t = (int)(quarter * 32 + lane);  // TMEM lane, also this thread's place in the group
+        const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + (uint32_t)(grp * C);
+        float* sc_buf = reinterpret_cast<float*>(smem + G::sc_off) + grp * 2 * C;
+        const int64_t row = lt * kF8Lanes + t, c0 = ct * NT + grp * C;
+        // scale addresses, clamped to rows that exist (the others' results are dropped)
+        const float* sl = p.sl + (int64_t)kb0 * p.ldsl + (p.l_tile ? lt : min64(row, p.RL - 1));
+        const float* sc = p.sc + (int64_t)kb0 * p.ldsc + min64(c0 + (t < C ? t : 0), p.RC - 1);
+        float acc[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+        bool ok = true;
+        int g = 0;
+        auto block = [&](float l, float s) {
+            const int buf = g & 1;
+            if (t < C) sc_buf[buf * C + t] = s;
+            bar_sync(1 + grp, 128);
+            if (ok) {  // once a wait has run out, the rest is skipped
+                ok = __all_sync(0xffffffffu, mbar_wait(accf + 8 * buf, (uint32_t)((g >> 1) & 1)));
+                if (!ok && lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
+            }
+            tc_fence_after();
+            if (ok) f8_accumulate<C, true>(taddr + NT * buf, l, sc_buf + buf * C, acc);
+            // this warp's reads of the buffer are done
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acce + 8 * buf);
+            ++g;
+        };
+        // two blocks a turn: the next two's scales are on their way meanwhile
+        auto lane_scale = [&](int kb) { return __ldg(sl + min(kb, kbs - 1) * p.ldsl); };
+        auto col_scale = [&](int kb) { return __ldg(sc + min(kb, kbs - 1) * p.ldsc); };
+        float l0 = lane_scale(0), l1 = lane_scale(1), s0 = col_scale(0), s1 = col_scale(1);
+#pragma unroll 1
+        for (int kb = 0; kb < kbs; kb += 2) {
+            const float m0 = lane_scale(kb + 2), m1 = lane_scale(kb + 3), n0 = col_scale(kb + 2), n1 = col_scale(kb + 3);
+            block(l0, s0);
+            if (kb + 1 < kbs) block(l1, s1);
+            l0 = m0;
+            l1 = m1;
+            s0 = n0;
+            s1 = n1;
+        }
+        if (p.split == 1) {
+            // lanes are consecutive columns of D: a warp writes runs of 32
+            if (row < p.RL) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (c0 + c < p.RC) f8_store(p, c0 + c, row, acc[c]);
+            }
+        } else {
+            // every block of this CTA has been read: the ring holds its partial sums now
+            float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+            for (int c = 0; c < C; ++c) part[(grp * C + c) * kF8Lanes + t] = acc[c];
+        }
+    }
+
+    if (p.split > 1) {
+        __syncthreads();
+        cluster_sync();
+        // rank r adds columns r, r + split, ... of the tile, rank 0's part first
+        if (warp >= 2) {
+            const int t = (int)((warp & 3) * 32 + lane);
+            const int64_t row = lt * kF8Lanes + t, c0 = ct * NT;
+            const uint32_t part = smem_u32(smem) + 4 * t;
+            // (the groups take turns of them)
+            const int grp = (int)(warp - 2) >> 2;
+            for (int c = rank + grp * p.split; c < NT && c0 + c < p.RC; c += G::groups * p.split) {
+                float v[kF8MaxSplit];
+#pragma unroll
+                for (int r = 0; r < kF8MaxSplit; ++r)
+                    v[r] = r < p.split ? ld_cluster(part + c * kF8Lanes * 4, r) : 0.0f;
+#pragma unroll
+                for (int r = 1; r < kF8MaxSplit; ++r) v[0] += v[r];
+                if (row < p.RL) f8_store(p, c0 + c, row, v[0]);
+            }
+        }
+        cluster_sync();  // no CTA leaves while another reads its sums
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, G::tmem_cols);
+    }
+}
+
+// ------------------------------------------------------------------ wide kernel
+
+// The wide kernel's register split: 384 threads start with 168 each; the first
+// warpgroup gives up 96 so that the two epilogue ones, which hold 128 sums per
+// thread, have 216 (72 + 2 * 216 = 3 * 168).
+constexpr int kF8RegsRoles = 72, kF8RegsEpilogue = 216;
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+struct F8Wide {
+    static constexpr int n = 256;                        // columns of a tile = rows of B
+    static constexpr int groups = 2;                     // epilogue groups of four warps
+    static constexpr int cols = n / groups;              // accumulator columns of a thread
+    static constexpr int first_epi = 4;                  // first epilogue warp (whole warpgroups, see kF8Regs)
+    static constexpr int threads = 32 * first_epi + 128 * groups;
+    static constexpr int stage_bytes = kF8LaneBytes + n * kFp8Block;
+    static constexpr int stages = 4;
+    static constexpr int stg_off = stages * stage_bytes; // 4 KiB of output staging per epilogue warp
+    static constexpr int sc_off = stg_off + 8 * 4096;    // column scales, two buffers per group
+    static constexpr int bar_off = sc_off + groups * 2 * cols * 4;
+    static constexpr int num_bars = 2 * stages + 5;
+    static constexpr int slot_off = bar_off + num_bars * 8;
+    static constexpr int smem = 896 + slot_off + 16;     // the base is 128-byte aligned, the ring 1024
+    static constexpr uint32_t tmem_cols = 2 * n;         // two buffers
+    static_assert(stage_bytes % 1024 == 0, "stages keep the 1024-byte alignment of the swizzle");
+    static_assert(smem <= 227 * 1024, "shared memory");
+};
+
+// VEC: B's scales are per row; else per 128 x 128 tile.
+template <bool VEC>
+__global__ void __launch_bounds__(F8Wide::threads, 1)
+    fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_l, const __grid_constant__ CUtensorMap map_c,
+                         const __grid_constant__ CUtensorMap map_d, const Fp8GemmParams p) {
+    using G = F8Wide;
+    constexpr int NT = G::n;
+    constexpr int S = G::stages, C = G::cols;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = align_shared<1024>(smem_raw);
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t full0 = smem_u32(smem + G::bar_off), empty0 = full0 + 8 * S;
+    const uint32_t accf = empty0 + 8 * S, acce = accf + 16, done_bar = acce + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::slot_off);
+
+    if (tid == 0) {
+        prefetch_tmap(&map_l);
+        prefetch_tmap(&map_c);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(accf + 8 * i, 1);
+            mbar_init(acce + 8 * i, 4 * G::groups);  // one arrival per epilogue warp
+        }
+        mbar_init(done_bar, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), G::tmem_cols);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int64_t unit = blockIdx.x, step = gridDim.x;
+    const int kbs = p.n_kb;
     const int64_t n_my = p.n_tiles > unit ? (p.n_tiles - 1 - unit) / step + 1 : 0;
 
     const int epi = (int)warp - G::first_epi;
@@ -233,7 +445,7 @@ __global__ void __launch_bounds__(F8Geo<NT>::threads, 1)
     const int grp = epi >> 2;
 
     if (epi < 0) {
-        if constexpr (G::wide) reg_dec<kF8RegsRoles>();
+        reg_dec<kF8RegsRoles>();
     }
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
@@ -252,8 +464,8 @@ __global__ void __launch_bounds__(F8Geo<NT>::threads, 1)
                 uint8_t* st = smem + s * G::stage_bytes;
                 const uint32_t bar = full0 + 8 * s;
                 mbar_arrive_expect_tx(bar, G::stage_bytes);
-                tma_load_2d(smem_u32(st), &map_l, (kb0 + kb) * kFp8Block, (int32_t)(lt * kF8Lanes), bar);
-                tma_load_2d(smem_u32(st + kF8LaneBytes), &map_c, (kb0 + kb) * kFp8Block, (int32_t)(ct * NT), bar);
+                tma_load_2d(smem_u32(st), &map_l, kb * kFp8Block, (int32_t)(lt * kF8Lanes), bar);
+                tma_load_2d(smem_u32(st + kF8LaneBytes), &map_c, kb * kFp8Block, (int32_t)(ct * NT), bar);
                 if (++s == S) {
                     s = 0;
                     ph ^= 1;
@@ -305,7 +517,7 @@ __global__ void __launch_bounds__(F8Geo<NT>::threads, 1)
         if (!mbar_wait(done_bar, 0) && one) atomicOr(&g_device_error, kErrWaitTimeout);
     } else if (epi >= 0) {
         // ------------------------------------------------ scale, accumulate, store
-        if constexpr (G::wide) reg_inc<kF8RegsEpilogue>();
+        reg_inc<kF8RegsEpilogue>();
         float acc[C];
         const int t = (int)quarter * 32 + (int)lane;  // TMEM lane, also this thread's place in the group
         const uint32_t taddr = tmem_base + ((quarter * 32u) << 16) + (uint32_t)(grp * C);
@@ -319,8 +531,8 @@ __global__ void __launch_bounds__(F8Geo<NT>::threads, 1)
             const int64_t lt = tile % p.n_lt, ct = tile / p.n_lt;
             const int64_t row = lt * kF8Lanes + t, c0 = ct * NT + grp * C;
             // scale addresses, clamped to rows that exist (the others' results are dropped)
-            const float* sl = p.sl + (int64_t)kb0 * p.ldsl + (p.l_tile ? lt : min64(row, p.RL - 1));
-            const float* sc = p.sc + (int64_t)kb0 * p.ldsc + (VEC ? min64(c0 + (t < C ? t : 0), p.RC - 1) : min64(c0, p.RC - 1) / kFp8Block);
+            const float* sl = p.sl + min64(row, p.RL - 1);
+            const float* sc = p.sc + (VEC ? min64(c0 + (t < C ? t : 0), p.RC - 1) : min64(c0, p.RC - 1) / kFp8Block);
 #pragma unroll
             for (int c = 0; c < C; ++c) acc[c] = 0.0f;
             auto lane_scale = [&](int kb) { return __ldg(sl + min(kb, kbs - 1) * p.ldsl); };
@@ -356,89 +568,48 @@ __global__ void __launch_bounds__(F8Geo<NT>::threads, 1)
                 s0 = t0;
                 s1 = t1;
             }
-            if constexpr (G::wide) {
-                if (p.tma_store) {
-                    // 32 rows x 128 bytes at a time through this warp's 4 KiB (128-byte swizzle)
-                    const uint32_t buf32 = smem_u32(smem + G::stg_off + stg);
+            if (p.tma_store) {
+                // 32 rows x 128 bytes at a time through this warp's 4 KiB (128-byte swizzle)
+                const uint32_t buf32 = smem_u32(smem + G::stg_off + stg);
 #pragma unroll
-                    for (int h = 0; h < C / 32; ++h) {  // boxes of 32 fp32 columns, or halves of 64 bf16 ones
-                        const bool first = !p.out_bf16 || (h & 1) == 0, last = !p.out_bf16 || (h & 1) == 1;
-                        if (first) {
-                            if (lane == 0) bulk_wait_read0();
-                            __syncwarp();
-                        }
-                        if (p.out_bf16) {
+                for (int h = 0; h < C / 32; ++h) {  // boxes of 32 fp32 columns, or halves of 64 bf16 ones
+                    const bool first = !p.out_bf16 || (h & 1) == 0, last = !p.out_bf16 || (h & 1) == 1;
+                    if (first) {
+                        if (lane == 0) bulk_wait_read0();
+                        __syncwarp();
+                    }
+                    if (p.out_bf16) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                sts_v4(buf32 + swz128(lane, 64 * (h & 1) + 16 * q),
-                                       bf16x2_pack(acc[32 * h + 8 * q], acc[32 * h + 8 * q + 1]),
-                                       bf16x2_pack(acc[32 * h + 8 * q + 2], acc[32 * h + 8 * q + 3]),
-                                       bf16x2_pack(acc[32 * h + 8 * q + 4], acc[32 * h + 8 * q + 5]),
-                                       bf16x2_pack(acc[32 * h + 8 * q + 6], acc[32 * h + 8 * q + 7]));
-                        } else {
+                        for (int q = 0; q < 4; ++q)
+                            sts_v4(buf32 + swz128(lane, 64 * (h & 1) + 16 * q),
+                                   bf16x2_pack(acc[32 * h + 8 * q], acc[32 * h + 8 * q + 1]),
+                                   bf16x2_pack(acc[32 * h + 8 * q + 2], acc[32 * h + 8 * q + 3]),
+                                   bf16x2_pack(acc[32 * h + 8 * q + 4], acc[32 * h + 8 * q + 5]),
+                                   bf16x2_pack(acc[32 * h + 8 * q + 6], acc[32 * h + 8 * q + 7]));
+                    } else {
 #pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                sts_v4(buf32 + swz128(lane, 16 * q), __float_as_uint(acc[32 * h + 4 * q]),
-                                       __float_as_uint(acc[32 * h + 4 * q + 1]), __float_as_uint(acc[32 * h + 4 * q + 2]),
-                                       __float_as_uint(acc[32 * h + 4 * q + 3]));
-                        }
-                        if (last) {
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            const int64_t col = c0 + 32 * h - (p.out_bf16 ? 32 : 0), r0 = lt * kF8Lanes + quarter * 32;
-                            if (lane == 0 && col < p.RC && r0 < p.RL) {
-                                tma_store_2d(&map_d, (int32_t)col, (int32_t)r0, buf32);
-                                bulk_commit();
-                            }
+                        for (int q = 0; q < 8; ++q)
+                            sts_v4(buf32 + swz128(lane, 16 * q), __float_as_uint(acc[32 * h + 4 * q]),
+                                   __float_as_uint(acc[32 * h + 4 * q + 1]), __float_as_uint(acc[32 * h + 4 * q + 2]),
+                                   __float_as_uint(acc[32 * h + 4 * q + 3]));
+                    }
+                    if (last) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        const int64_t col = c0 + 32 * h - (p.out_bf16 ? 32 : 0), r0 = lt * kF8Lanes + quarter * 32;
+                        if (lane == 0 && col < p.RC && r0 < p.RL) {
+                            tma_store_2d(&map_d, (int32_t)col, (int32_t)r0, buf32);
+                            bulk_commit();
                         }
                     }
-                } else if (row < p.RL) {
-#pragma unroll
-                    for (int c = 0; c < C; ++c)
-                        if (c0 + c < p.RC) f8_store(p, row, c0 + c, acc[c]);
                 }
-            } else {
-                if (p.split == 1) {
-                    // lanes are consecutive columns of D: a warp writes runs of 32
-                    if (row < p.RL) {
+            } else if (row < p.RL) {
 #pragma unroll
-                        for (int c = 0; c < C; ++c)
-                            if (c0 + c < p.RC) f8_store(p, c0 + c, row, acc[c]);
-                    }
-                } else {
-                    // every block of this CTA has been read: the ring holds its partial sums now
-                    float* part = reinterpret_cast<float*>(smem);
-#pragma unroll
-                    for (int c = 0; c < C; ++c) part[c * kF8Lanes + t] = acc[c];
-                }
+                for (int c = 0; c < C; ++c)
+                    if (c0 + c < p.RC) f8_store(p, row, c0 + c, acc[c]);
             }
         }
-        if constexpr (G::wide) {
-            if (lane == 0) bulk_wait0();
-        }
-    }
-
-    if constexpr (!G::wide) {
-        if (p.split > 1) {
-            __syncthreads();
-            cluster_sync();
-            // rank r adds columns r, r + split, ... of the tile, rank 0's part first
-            if (epi >= 0) {
-                const int t = (int)quarter * 32 + (int)lane;
-                const int64_t row = (unit % p.n_lt) * kF8Lanes + t, c0 = unit / p.n_lt * NT;
-                const uint32_t part = smem_u32(smem) + 4 * t;
-                for (int c = (int)rank; c < C && c0 + c < p.RC; c += p.split) {
-                    float v[kF8MaxSplit];
-#pragma unroll
-                    for (int r = 0; r < kF8MaxSplit; ++r)
-                        v[r] = r < p.split ? ld_cluster(part + c * kF8Lanes * 4, r) : 0.0f;
-#pragma unroll
-                    for (int r = 1; r < kF8MaxSplit; ++r) v[0] += v[r];
-                    if (row < p.RL) f8_store(p, c0 + c, row, v[0]);
-                }
-            }
-            cluster_sync();  // no CTA leaves while another reads its sums
-        }
+        if (lane == 0) bulk_wait0();
     }
 
     tc_fence_before();

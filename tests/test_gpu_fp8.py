@@ -156,10 +156,10 @@ def test_gemm_scales_differ_by_block(fq, M):
     check(fq.gemm_fp8(*a, *b, fq.FP4Q_FP8_ROW, torch.float32), *reference(a, b, False), K, "scales")
 
 
-@pytest.mark.parametrize("M", [1, 20, 200])
+@pytest.mark.parametrize("M,N", [(1, 130), (20, 130), (200, 130), (200, 128), (200, 132), (300, 129)])
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
-def test_gemm_writes_only_its_output(fq, M, out):
-    N, K = 130, 200
+def test_gemm_writes_only_its_output(fq, M, N, out):
+    K = 200
     a, b = operands(fq, M, N, K, True, 11)
     for ldd in (144, 137):  # rows 16 bytes apart in step, and not
         buf = torch.full((M + 2, ldd), 123.0, dtype=out, device="cuda").contiguous()
