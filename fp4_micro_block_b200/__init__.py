@@ -300,6 +300,7 @@ def _want(t, name, dtypes, *shape):
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+_NO_SIZE = C.c_size_t(-1).value
 _KV = struct.Struct("<5q3i4x2q")  # fp4q_kv_cache
 
 
@@ -318,9 +319,17 @@ def _fp8_rows(n, block):
 
 def _fp8_side(codes, scales, rows, cols, block, what):
     """Codes [rows, cols] and scales [ceil(cols/128), rows or tile rows]: their strides."""
-    _want(codes, what, _CODES, rows, cols)
-    _want(scales, what, _F32, -(-cols // 128), _fp8_rows(rows, block))
-    return _row_stride(codes, what, 16), _row_stride(scales, what, 4)
+    n = rows if block == FP4Q_FP8_ROW else -(-rows // 128)
+    kb = -(-cols // 128)
+    if codes.dtype not in _CODES or scales.dtype is not torch.float32 or codes.shape != (rows, cols) or scales.shape != (kb, n):
+        _want(codes, what, _CODES, rows, cols)
+        _want(scales, what, _F32, kb, n)
+    ld, step = codes.stride()
+    lds, steps = scales.stride()
+    if (step != 1 and cols > 1) or (steps != 1 and n > 1):
+        raise ValueError(f"{what} must be row-major views (unit column stride)")
+    # (a single row's stride says nothing)
+    return ld if rows > 1 else -(-cols // 16) * 16, lds if kb > 1 else -(-n // 4) * 4
 
 
 def fp4q_quantize_fp8(x, block, codes=None, scales=None, codes_t=None, scales_t=None, stream=None):
@@ -342,7 +351,9 @@ def fp4q_quantize_fp8(x, block, codes=None, scales=None, codes_t=None, scales_t=
 
 def fp4q_gemm_fp8(a_codes, a_scales, b_codes, b_scales, b_block, d, stream=None):
     """d [M, N] (float32 or bfloat16) = A B^T of two fp4q_quantize_fp8 outputs (A: row blocks)."""
-    _want(d, "d", (torch.float32, torch.bfloat16), None, None)
+    bf16 = d.dtype is torch.bfloat16
+    if not bf16 or len(d.shape) != 2:
+        _want(d, "d", (torch.float32, torch.bfloat16), None, None)
     M, N = d.shape
     K = a_codes.shape[-1]
     dev = _device("fp4q_gemm_fp8", d, a_codes, a_scales, b_codes, b_scales)
@@ -350,58 +361,61 @@ def fp4q_gemm_fp8(a_codes, a_scales, b_codes, b_scales, b_block, d, stream=None)
     ldb, ldbs = _fp8_side(b_codes, b_scales, N, K, b_block, "B's codes / scales")
     return _launch("fp4q_gemm_fp8", dev, _lib.fp4q_gemm_fp8,
                    (a_codes.data_ptr(), lda, a_scales.data_ptr(), ldas, b_codes.data_ptr(), ldb, b_scales.data_ptr(), ldbs,
-                    b_block, M, N, K, d.data_ptr(), _row_stride(d, "d", 1), d.dtype is torch.bfloat16), stream)
-
-
-def _token_stride(t, name):
-    """Stride between tokens of [tokens, heads, dim] whose heads and dims are contiguous."""
-    T, H, D = t.shape
-    st, sh, sd = t.stride()
-    if (D > 1 and sd != 1) or (H > 1 and sh != D):
-        raise ValueError(f"{name}: heads and dims of a token must be contiguous")
-    return st if T > 1 else H * D
+                    b_block, M, N, K, d.data_ptr(), _row_stride(d, "d", 1), bf16), stream)
 
 
 def _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table):
-    """The bytes of an fp4q_kv_cache, its head count and head dim."""
-    _want(k_cache, "k_cache", _CODES, None, None, None, None)
-    pages, heads, page, dim = k_cache.shape
-    _want(v_cache, "v_cache", _CODES, pages, heads, page, dim)
-    _want(k_scale, "k_scale", _F32, pages, heads)
-    _want(v_scale, "v_scale", _F32, pages, heads)
-    _want(block_table, "block_table", _I32, None, None)
+    """The bytes of an fp4q_kv_cache, its head count, head dim and batch."""
+    shape = k_cache.shape
+    if (len(shape) != 4 or v_cache.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2] or
+            len(block_table.shape) != 2 or k_cache.dtype not in _CODES or v_cache.dtype not in _CODES or
+            k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32 or block_table.dtype is not torch.int32):
+        _want(k_cache, "k_cache", _CODES, None, None, None, None)
+        _want(v_cache, "v_cache", _CODES, *shape)
+        _want(k_scale, "k_scale", _F32, *shape[:2])
+        _want(v_scale, "v_scale", _F32, *shape[:2])
+        _want(block_table, "block_table", _I32, None, None)
     if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and
             v_scale.is_contiguous() and block_table.is_contiguous()):
         raise ValueError("the cache, its scales and the block table must be contiguous")
+    pages, heads, page, dim = shape
+    B, width = block_table.shape
     return _KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads, page,
-                    dim, block_table.data_ptr(), block_table.shape[1]), heads, dim
+                    dim, block_table.data_ptr(), width), heads, dim, B
 
 
-def _ragged(cu, lens, block_table, name):
-    B = block_table.shape[0]
-    _want(cu, name, _I32, B + 1)
-    _want(lens, "lens", _I32, B)
+def _ragged(cu, lens, B, name):
+    if cu.dtype is not torch.int32 or lens.dtype is not torch.int32 or cu.shape != (B + 1,) or lens.shape != (B,):
+        _want(cu, name, _I32, B + 1)
+        _want(lens, "lens", _I32, B)
     if not (cu.is_contiguous() and lens.is_contiguous()):
         raise ValueError(f"{name} and lens must be contiguous")
-    return B
+
+
+def _tokens(t, name, T, heads, dim):
+    """bf16 [T, heads, dim] whose heads and dims are contiguous: the stride between tokens."""
+    if t.dtype is not torch.bfloat16 or t.shape != (T, heads, dim):
+        _want(t, name, _BF16, T, heads, dim)
+    st, sh, sd = t.stride()
+    if (dim > 1 and sd != 1) or (heads > 1 and sh != dim):
+        raise ValueError(f"{name}: heads and dims of a token must be contiguous")
+    return st if T > 1 else heads * dim
 
 
 def fp4q_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, lens, max_new, stream=None):
     """Writes the new tokens k, v [tokens, Hkv, D] (bf16) at the end of their sequences."""
     dev = _device("fp4q_kv_append_fp8", k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, lens)
-    cache, heads, dim = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+    cache, heads, dim, B = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table)
     T = k.shape[0]
-    _want(k, "k", _BF16, T, heads, dim)
-    _want(v, "v", _BF16, T, heads, dim)
-    B = _ragged(cu_new, lens, block_table, "cu_new")
+    ldk, ldv = _tokens(k, "k", T, heads, dim), _tokens(v, "v", T, heads, dim)
+    _ragged(cu_new, lens, B, "cu_new")
     return _launch("fp4q_kv_append_fp8", dev, _lib.fp4q_kv_append_fp8,
-                   (k.data_ptr(), _token_stride(k, "k"), v.data_ptr(), _token_stride(v, "v"), T, cache,
-                    cu_new.data_ptr(), lens.data_ptr(), B, max_new), stream)
+                   (k.data_ptr(), ldk, v.data_ptr(), ldv, T, cache, cu_new.data_ptr(), lens.data_ptr(), B, max_new), stream)
 
 
 def fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, num_q_heads, num_kv_heads, head_dim):
-    n = int(_lib.fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, num_q_heads, num_kv_heads, head_dim))
-    if n == C.c_size_t(-1).value:
+    n = _lib.fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, num_q_heads, num_kv_heads, head_dim)
+    if n == _NO_SIZE:
         raise Fp4qError(FP4Q_ERR_INVALID_ARG, "fp4q_attention_fp8_workspace_bytes")
     return n
 
@@ -410,21 +424,18 @@ def fp4q_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q,
                        causal=True, softmax_scale=None, workspace=None, stream=None):
     """o [tokens, Hq, D] (bf16) = attention of q [tokens, Hq, D] (bf16) over the cache."""
     dev = _device("fp4q_attention_fp8", q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, o, lse, workspace)
-    cache, _, dim = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table)
-    T, Hq, D = q.shape
-    _want(q, "q", _BF16, T, Hq, dim)
-    _want(o, "o", _BF16, T, Hq, dim)
-    B = _ragged(cu_q, lens, block_table, "cu_q")
-    if lse is not None:
+    cache, _, dim, B = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+    T, Hq, _ = q.shape
+    ldq, ldo = _tokens(q, "q", T, Hq, dim), _tokens(o, "o", T, Hq, dim)
+    _ragged(cu_q, lens, B, "cu_q")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()):
         _want(lse, "lse", _F32, T, Hq)
-        if not lse.is_contiguous():
-            raise ValueError("lse must be contiguous")
-    scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
+        raise ValueError("lse must be contiguous")
+    scale = dim ** -0.5 if softmax_scale is None else float(softmax_scale)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return _launch("fp4q_attention_fp8", dev, _lib.fp4q_attention_fp8,
-                   (q.data_ptr(), _token_stride(q, "q"), T, Hq, cache, cu_q.data_ptr(), lens.data_ptr(), B, max_q,
-                    max_len, bool(causal), scale, o.data_ptr(), _token_stride(o, "o"),
-                    None if lse is None else lse.data_ptr(), ws, ws_bytes), stream)
+                   (q.data_ptr(), ldq, T, Hq, cache, cu_q.data_ptr(), lens.data_ptr(), B, max_q, max_len, bool(causal),
+                    scale, o.data_ptr(), ldo, None if lse is None else lse.data_ptr(), ws, ws_bytes), stream)
 
 
 # ----------------------------------------------------------------------------- allocating helpers
@@ -568,16 +579,21 @@ def kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_new,
 
 def attention_fp8_workspace(q, k_cache, batch, max_q, max_len):
     """Scratch for attention_fp8 calls of these sizes (None: none is needed)."""
-    with torch.cuda.device(q.device):
-        n = fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, q.shape[1], k_cache.shape[1], k_cache.shape[3])
+    sizes = (batch, max_q, max_len, q.shape[1], k_cache.shape[1], k_cache.shape[3])
+    if torch._C._cuda_getDevice() == q.get_device():
+        n = fp4q_attention_fp8_workspace_bytes(*sizes)
+    else:
+        with torch.cuda.device(q.device):
+            n = fp4q_attention_fp8_workspace_bytes(*sizes)
     return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
 
 
 def attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, max_q, max_len, causal=True,
                   softmax_scale=None, ws=None):
     """(o [tokens, Hq, D] bf16, lse [tokens, Hq] f32); tokens that belong to no sequence are left unset."""
-    o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    T, Hq, D = q.shape
+    o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     if ws is None:
         ws = attention_fp8_workspace(q, k_cache, block_table.shape[0], max_q, max_len)
     fp4q_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, max_q, max_len, o, lse, causal,

@@ -98,7 +98,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // What one split leaves for the others: rows of D sums, then the row's maximum
-// and denominator, in the workspace (one slot per row of a row tile and split).
+// and denominator.  Up to eight splits of a row tile are a cluster, whose CTAs
+// read each other's slots in shared memory; the slots of more are in the
+// workspace, for a second kernel.
 template <int D>
 constexpr int kAttnSlot = D + 2;
 
@@ -109,7 +111,7 @@ struct AttnSplit {
     uint32_t row_tiles, splits;
     int32_t chunk;      // keys per split, a multiple of 128
     uint32_t slot_rows; // rows of a tile that may exist: min(16, max_q * G)
-    float* ws;          // NULL: one split
+    float* ws;          // NULL: one split, or a cluster of them
 };
 
 // Smallest v such that keys >= v of the row are masked.
@@ -163,8 +165,10 @@ struct AttnGeo {
     static constexpr int stage_bytes = 2 * tile_bytes;
     static constexpr int ring = warps * stages * stage_bytes;
     static constexpr int pages = kAttnMaxChunk / 16;
-    static constexpr int red = warps * kAttnRows * (D + 4) * 4;  // the warps' sums, in the ring's place
-    static constexpr int qf_off = ring > red ? ring : red;
+    // in the ring's place at the end: the warps' sums, and this split's slots for a cluster
+    static constexpr int red = warps * kAttnRows * (D + 4) * 4;
+    static constexpr int slots = red + kAttnRows * kAttnSlot<D> * 4;
+    static constexpr int qf_off = ring > slots ? ring : slots;
     static constexpr int ids_off = qf_off + D / 16 * 32 * 16;
     static constexpr int ml_off = ids_off + 4 * 4 * pages;
     static constexpr int bar_off = ml_off + 2 * 4 * warps * kAttnRows;
@@ -246,7 +250,8 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
     // keys this tile sees (the last row sees most), and this split's part of them
     const int most = attn_limit(p, s, r0 + rows - 1);
     const int k0 = (int)min64((int64_t)split * sp.chunk, most), k1 = min(most - k0, sp.chunk) + k0;
-    if (split > 0 && k0 >= k1) return;
+    const bool joined = sp.splits > 1 && !sp.ws;  // a cluster: every CTA of it stays to the end
+    if (split > 0 && k0 >= k1 && !joined) return;
     const int every = attn_limit(p, s, r0);  // keys below are seen by every row of the tile
     const int lim0 = attn_limit(p, s, r0 + g), lim1 = attn_limit(p, s, r0 + g + 8);
 
@@ -496,8 +501,8 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) v[d] += red[(w * kAttnRows + r) * (D + 4) + lane * (D / 32) + d];
         }
-        if (sp.ws) {
-            float* slot = sp.ws + ((((int64_t)(b * p.c.heads + hk) * sp.row_tiles + rt) * sp.slot_rows + r) * sp.splits + split) * kAttnSlot<D>;
+        if (sp.splits > 1) {
+            float* slot = joined ? red + G::red / 4 + r * kAttnSlot<D> : sp.ws + ((((int64_t)(b * p.c.heads + hk) * sp.row_tiles + rt) * sp.slot_rows + r) * sp.splits + split) * kAttnSlot<D>;
 #pragma unroll
             for (int d = 0; d < D / 32; ++d) slot[lane * (D / 32) + d] = v[d];
             if (lane == 0) {
@@ -513,6 +518,36 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
             for (int d = 0; d < D / 32; d += 2) dst[d / 2] = bf16x2_pack(v[d] * inv, v[d + 1] * inv);
             if (p.lse && lane == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
         }
+    }
+    if (joined) {
+        cluster_sync();
+        // CTA i of the cluster finishes rows i, i + splits, ..; a warp a row, a lane D / 32 dims
+        for (int r = (int)split + warp * (int)sp.splits; r < rows; r += kWarps * (int)sp.splits) {
+            const uint32_t slot = smem_u32(red) + G::red + r * kAttnSlot<D> * 4;
+            float m[8], z[8], top = -INFINITY, l = 0.0f, v[D / 32] = {};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                m[i] = i < (int)sp.splits ? ld_cluster(slot + 4 * D, i) : -INFINITY;
+                z[i] = i < (int)sp.splits ? ld_cluster(slot + 4 * D + 4, i) : 0.0f;
+                top = fmaxf(top, m[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i >= (int)sp.splits) break;
+                const float a = m[i] == -INFINITY ? 1.0f : exp2_approx(m[i] - top);
+                l = fmaf(z[i], a, l);
+#pragma unroll
+                for (int d = 0; d < D / 32; ++d) v[d] = fmaf(ld_cluster(slot + 4 * (lane * (D / 32) + d), i), a, v[d]);
+            }
+            const uint32_t row = r0 + r, i = row / (uint32_t)p.group;
+            const int64_t tok = s.first + i, h = hk * p.group + (row - i * p.group);
+            const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + lane * (D / 32));
+#pragma unroll
+            for (int d = 0; d < D / 32; d += 2) dst[d / 2] = bf16x2_pack(v[d] * inv, v[d + 1] * inv);
+            if (p.lse && lane == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+        }
+        cluster_sync();  // no CTA leaves while another reads its slots
     }
 }
 

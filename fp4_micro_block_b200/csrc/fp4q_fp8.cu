@@ -335,13 +335,15 @@ namespace {
 // where there are too few tiles to fill the GPU (by the lengths' bound, since
 // the lengths are on the device).
 struct AttnPlan {
-    bool tile;  // attn_tile_kernel
+    bool tile;     // attn_tile_kernel
+    bool cluster;  // the splits of a row tile join within a cluster
     int64_t row_tiles, splits, chunk, slot_rows;
     size_t ws_bytes;
 };
 
 constexpr int64_t kAttnMost = (int64_t)1 << 30;
 constexpr int64_t kAttnTileFrom = 64;
+constexpr int64_t kAttnCluster = 8;
 
 fp4q_status attn_plan(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_heads, int64_t kv_heads, int64_t dim,
                       int sms, AttnPlan* out) {
@@ -358,11 +360,17 @@ fp4q_status attn_plan(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_h
     }
     a.slot_rows = std::min<int64_t>(kAttnRows, max_q * (q_heads / kv_heads));
     const int64_t items = batch * kv_heads * a.row_tiles;
+    // three CTAs fit on an SM
     const int64_t want = std::max<int64_t>(1, spans(3 * (int64_t)sms, items));
     a.chunk = std::min<int64_t>(kAttnMaxChunk, std::max<int64_t>(128, spans(spans(max_len, want), 128) * 128));
     a.splits = std::max<int64_t>(1, spans(max_len, a.chunk));
+    // A cluster saves the second launch (4 us of the host's time, none of the GPU's)
+    // but holds its CTAs until the last is done: 32 x 8192 keys in clusters of two
+    // took 111 us, with the second kernel 85.  So only where all have an SM to
+    // themselves.
+    a.cluster = a.splits > 1 && a.splits <= kAttnCluster && items * a.splits <= sms;
     if (a.splits >= kMaxDim / items || items >= kMaxDim / kAttnRows) return FP4Q_ERR_UNSUPPORTED;
-    a.ws_bytes = a.splits > 1 ? (size_t)(items * a.splits * a.slot_rows * (dim + 2)) * sizeof(float) : 0;
+    a.ws_bytes = a.splits > 1 && !a.cluster ? (size_t)(items * a.splits * a.slot_rows * (dim + 2)) * sizeof(float) : 0;
     *out = a;
     return FP4Q_OK;
 }
@@ -398,7 +406,7 @@ fp4q_status launch_attn_tile(const AttnParams& p, const AttnPlan& a, cudaStream_
 template <int D>
 fp4q_status launch_attn(const AttnParams& p, const AttnPlan& a, void* ws, cudaStream_t s) {
     using G = AttnGeo<D>;
-    AttnSplit sp{(uint32_t)a.row_tiles, (uint32_t)a.splits, (int32_t)a.chunk, (uint32_t)a.slot_rows, a.splits > 1 ? static_cast<float*>(ws) : nullptr};
+    AttnSplit sp{(uint32_t)a.row_tiles, (uint32_t)a.splits, (int32_t)a.chunk, (uint32_t)a.slot_rows, a.ws_bytes > 0 ? static_cast<float*>(ws) : nullptr};
     auto kern = attn_rows_kernel<D>;
     static std::atomic<uint64_t> done{0};
     fp4q_status st = ensure_smem(kern, G::smem, done);
@@ -406,8 +414,8 @@ fp4q_status launch_attn(const AttnParams& p, const AttnPlan& a, void* ws, cudaSt
     CUtensorMap map_k, map_v;
     if ((st = make_kv_map(&map_k, p.c, p.c.k)) != FP4Q_OK || (st = make_kv_map(&map_v, p.c, p.c.v)) != FP4Q_OK) return st;
     const int64_t items = p.batch * p.c.heads * a.row_tiles;
-    st = launch(kern, (int)(items * a.splits), 32 * G::warps, G::smem, s, map_k, map_v, p, sp);
-    if (st != FP4Q_OK || a.splits == 1) return st;
+    st = launch_cluster(kern, items * a.splits, a.cluster ? (int)a.splits : 1, 32 * G::warps, G::smem, s, map_k, map_v, p, sp);
+    if (st != FP4Q_OK || a.ws_bytes == 0) return st;
     return launch(attn_join_kernel<D>, (int)(items * a.slot_rows), 128, 0, s, p, sp);
 }
 

@@ -38,6 +38,19 @@ __device__ __forceinline__ Half4 e4m3x4_f16(uint32_t four) {
     return h;
 }
 
+// All CTAs of the cluster have arrived, and see each other's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The float at shared-memory address `saddr` of the cluster's CTA `rank`.
+__device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
 // A pair of fp32 values and operations on both (each rounded as alone).
 __device__ __forceinline__ uint64_t f2_pack(uint32_t lo, uint32_t hi) {
     uint64_t r;

@@ -126,7 +126,9 @@ def test_binding_refuses_host_tensors_wrong_types_and_shapes(fq):
     with pytest.raises(ValueError):
         fq._kv_cache(*cache, torch.zeros((1, 2), dtype=torch.int64))
     with pytest.raises(ValueError):
-        fq._token_stride(torch.zeros((2, 4, 64)).transpose(0, 1), "q")
-    assert fq._token_stride(torch.zeros((5, 8, 64))[:, 2:4], "q") == 512
+        fq._tokens(torch.zeros((2, 4, 64), dtype=torch.bfloat16).transpose(0, 1), "q", 4, 2, 64)
+    with pytest.raises(ValueError):
+        fq._tokens(torch.zeros((2, 4, 64)), "q", 2, 4, 64)
+    assert fq._tokens(torch.zeros((5, 8, 64), dtype=torch.bfloat16)[:, 2:4], "q", 5, 2, 64) == 512
     c = fq.Fp4qKvCache(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
     assert bytes(c) == fq._KV.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
