@@ -342,16 +342,29 @@ struct AttnPlan {
 };
 
 constexpr int64_t kAttnMost = (int64_t)1 << 30;
-constexpr int64_t kAttnTileFrom = 64;
 constexpr int64_t kAttnCluster = 8;
+
+// Whether attn_tile_kernel (128 rows a CTA) is the faster one, by what it and
+// attn_rows_kernel (16 rows) took on one B200 at D = 128, in ns: 7000 and 1550 a
+// wave and 128 keys against 6000, 18 a key for each of the 3 CTAs an SM holds,
+// and 64 a row tile for the join where the keys are split.  Measured, in us (tile
+// / rows), 8 K/V heads of 4: 32 queries over 512 keys 13.9 / 13.1, 64 over 512
+// 14.0 / 19.7, 64 over 4096 53.6 / 41.6, 128 over 4096 53.8 / 64.1, two of 400
+// over 4096 95 / 208; 16 sequences of 8 queries in groups of 8 over 2000 31 / 47.
+bool attn_take_tile(int64_t row_items, int64_t tile_items, int64_t max_len, int64_t rows, int sms) {
+    if (rows <= kAttnRows) return false;
+    const double by_rows = 6000.0 + 18.0 * row_items * max_len / (3.0 * sms) + (row_items < 3 * (int64_t)sms ? 64.0 * row_items : 0.0);
+    const double by_tile = 7000.0 + 1550.0 * spans(tile_items, sms) * spans(max_len, kTileKeys);
+    return by_tile < by_rows;
+}
 
 fp4q_status attn_plan(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_heads, int64_t kv_heads, int64_t dim,
                       int sms, AttnPlan* out) {
     AttnPlan a{};
     // rows and keys are counted in 31 bits, with room for the last tile
     if (max_len > kAttnMost || max_q > kAttnMost / (q_heads / kv_heads)) return FP4Q_ERR_UNSUPPORTED;
-    const int64_t rows = max_q * (q_heads / kv_heads);
-    a.tile = dim <= 128 && rows >= kAttnTileFrom;
+    const int64_t rows = max_q * (q_heads / kv_heads), heads = batch * kv_heads;
+    a.tile = dim <= 128 && attn_take_tile(heads * spans(rows, kAttnRows), heads * spans(rows, kTileRows), max_len, rows, sms);
     a.row_tiles = spans(rows, a.tile ? kTileRows : kAttnRows);
     if (a.row_tiles >= kMaxDim / kv_heads || a.row_tiles * kv_heads >= kMaxDim / batch) return FP4Q_ERR_UNSUPPORTED;
     if (a.tile) {
