@@ -410,11 +410,11 @@ def fp4q_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu
     ldk, ldv = _tokens(k, "k", T, heads, dim), _tokens(v, "v", T, heads, dim)
     _ragged(cu_new, lens, B, "cu_new")
     return _launch("fp4q_kv_append_fp8", dev, _lib.fp4q_kv_append_fp8,
-                   (k.data_ptr(), ldk, v.data_ptr(), ldv, T, cache, cu_new.data_ptr(), lens.data_ptr(), B, max_new), stream)
+                   (k.data_ptr(), ldk, v.data_ptr(), ldv, T, cache, cu_new.data_ptr(), lens.data_ptr(), B, int(max_new)), stream)
 
 
 def fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, num_q_heads, num_kv_heads, head_dim):
-    n = _lib.fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, num_q_heads, num_kv_heads, head_dim)
+    n = _lib.fp4q_attention_fp8_workspace_bytes(int(batch), int(max_q), int(max_len), num_q_heads, num_kv_heads, head_dim)
     if n == _NO_SIZE:
         raise Fp4qError(FP4Q_ERR_INVALID_ARG, "fp4q_attention_fp8_workspace_bytes")
     return n
@@ -434,7 +434,7 @@ def fp4q_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q,
     scale = dim ** -0.5 if softmax_scale is None else float(softmax_scale)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return _launch("fp4q_attention_fp8", dev, _lib.fp4q_attention_fp8,
-                   (q.data_ptr(), ldq, T, Hq, cache, cu_q.data_ptr(), lens.data_ptr(), B, max_q, max_len, bool(causal),
+                   (q.data_ptr(), ldq, T, Hq, cache, cu_q.data_ptr(), lens.data_ptr(), B, int(max_q), int(max_len), bool(causal),
                     scale, o.data_ptr(), ldo, None if lse is None else lse.data_ptr(), ws, ws_bytes), stream)
 
 

@@ -270,3 +270,24 @@ def test_quantized_nvfp4_workload_values(fq):
     got = fq.quantize_fp8(x)
     want = fp8.quantize(host(x), False)
     assert np.array_equal(to_np(got[0]), want[0]) and np.array_equal(to_np(got[1]), want[1])
+
+
+def test_offsets_past_32_bits(fq):
+    """More than 2^31 elements of x, codes and D: the last rows are those of a call on them alone."""
+    M, K, N, last = 1_050_112, 2056, 2056, 4096  # whole blocks of 128 rows
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    x[:-last].fill_(1.0)
+    x[-last:] = activations(last, K, 51)
+    assert x.numel() > 2 ** 31
+    for block, rows in ((fq.FP4Q_FP8_ROW, last), (fq.FP4Q_FP8_TILE, last // 128)):
+        whole, part = fq.quantize_fp8(x, block, True), fq.quantize_fp8(x[-last:], block, True)
+        assert torch.equal(whole[0][-last:], part[0]) and torch.equal(whole[1][:, -rows:], part[1])
+        assert torch.equal(whole[2][:, -last:], part[2]) and torch.equal(whole[3][-last // 128:], part[3])
+        if block == fq.FP4Q_FP8_ROW:
+            a, alone = whole[:2], part[:2]
+    alone_rows = fq.quantize_fp8(x)
+    assert torch.equal(alone_rows[0], a[0]) and torch.equal(alone_rows[1], a[1])
+    del whole, alone_rows, x
+    w = fq.quantize_fp8(activations(N, K, 52), fq.FP4Q_FP8_TILE)
+    D = fq.gemm_fp8(*a, *w)
+    assert D.numel() > 2 ** 31 and torch.equal(D[-last:], fq.gemm_fp8(*alone, *w))

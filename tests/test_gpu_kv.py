@@ -589,3 +589,31 @@ def test_batches_of_chunks_in_a_graph_and_on_two_streams(fq):
     torch.cuda.synchronize()
     for a, b in outs:
         assert torch.equal(a, o) and torch.equal(b, lse)
+
+
+@pytest.mark.parametrize("new,B", [(1, 3), (48, 16)])
+def test_offsets_past_32_bits(fq, new, B):
+    """Pages whose codes lie more than 2^31 bytes into the cache: the same bits as from a small cache."""
+    rng = np.random.default_rng(41)
+    heads, page, D, G, L = 8, 128, 128, 2, 300
+    small_pool, big_pool = 3 * B, 17000
+    shift = big_pool - small_pool
+    cu = cum([new] * B)
+    q, k, v = bf16(rng, cu[-1], heads * G, D), bf16(rng, cu[-1], heads, D), bf16(rng, cu[-1], heads, D)
+    start = up(random_cache(rng, small_pool, heads, page, D))
+    for s in start[2:]:
+        s.copy_(torch.exp2(torch.floor(torch.log2(s))))
+    table = rng.permutation(small_pool).reshape(B, 3).astype(np.int32)
+    small = [t.clone() for t in start]
+    big = [torch.empty((big_pool, *t.shape[1:]), dtype=t.dtype, device="cuda") for t in start]
+    for t, b in zip(start, big):
+        b[shift:] = t
+    outs = []
+    for cache, tab in ((small, table), (big, table + shift)):
+        args = (i32(tab.tolist()), i32(cu), i32([L] * B))
+        fq.kv_append_fp8(k, v, *cache, *args, new)
+        outs.append(fq.attention_fp8(q, *cache, *args, new, L))
+    assert big[0].numel() > 2 ** 31
+    for a, b in zip(small, big):
+        assert torch.equal(a, b[shift:])
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
