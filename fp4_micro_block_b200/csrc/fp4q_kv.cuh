@@ -116,20 +116,27 @@ __global__ void __launch_bounds__(kKvMaxThreads) kv_append_kernel(const KvAppend
             *at = old > 0.0f ? make_uint2(e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7])) : make_uint2(0, 0);
         }
     }
-    const bool exact = (__float_as_uint(s) & 0x7fffffu) == 0;  // a power of two, as this kernel writes it
+    uint8_t* dst = codes + ((int64_t)from << (p.per_row_log2 + 3));
+    if ((__float_as_uint(s) & 0x7fffffu) == 0) {  // a power of two, as this kernel writes it: exact products
+        const uint64_t inv2 = f2_both(inv);
 #pragma unroll
-    for (int k = 0; k < kKvPieces; ++k) {
-        const int e = threadIdx.x + k * blockDim.x;
-        if (e >= count) break;
-        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-        float f[8];
+        for (int k = 0; k < kKvPieces; ++k) {
+            const int e = threadIdx.x + k * blockDim.x;
+            if (e >= count) break;
+            const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+            uint64_t f[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            f[2 * t] = exact ? bf16lo(u[t]) * inv : __fdiv_rn(bf16lo(u[t]), s);
-            f[2 * t + 1] = exact ? bf16hi(u[t]) * inv : __fdiv_rn(bf16hi(u[t]), s);
+            for (int t = 0; t < 4; ++t) f[t] = f2_mul(f2_pack(u[t] << 16, u[t] & 0xffff0000u), inv2);
+            *reinterpret_cast<uint2*>(dst + (int64_t)e * 8) =
+                make_uint2(e4m3_pack4(f2_lo(f[0]), f2_hi(f[0]), f2_lo(f[1]), f2_hi(f[1])),
+                           e4m3_pack4(f2_lo(f[2]), f2_hi(f[2]), f2_lo(f[3]), f2_hi(f[3])));
         }
-        *reinterpret_cast<uint2*>(codes + ((int64_t)from << (p.per_row_log2 + 3)) + (int64_t)e * 8) =
-            make_uint2(e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7]));
+    } else {  // a calibrated scale of the caller's
+#pragma unroll 1
+        for (int e = threadIdx.x; e < count; e += blockDim.x) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(rows + (e >> p.per_row_log2) * ld + (e & mask) * 8));
+            *reinterpret_cast<uint2*>(dst + (int64_t)e * 8) = make_uint2(fp8_codes_ieee(x.x, x.y, s), fp8_codes_ieee(x.z, x.w, s));
+        }
     }
 }
 

@@ -143,6 +143,22 @@ def test_append_strided_and_extreme_values(fq):
     assert float(dev[2][4, 0]) == 2.0 ** 120 and int(dev[0][4, 0, 0, 0]) == 0x7E
 
 
+def test_append_to_pages_with_scales_that_are_no_powers_of_two(fq):
+    """A page that carries a calibrated scale keeps it while it suffices, and moves to a power of two where it does not."""
+    rng = np.random.default_rng(8)
+    page, D, heads = 32, 64, 2
+    cache = random_cache(rng, 4, heads, page, D)
+    for s in cache[2:]:
+        s[:] = np.float32(0.013) * np.float32([[1], [3], [0.1], [1]])
+    table = np.array([[0], [1], [2]], np.int32)
+    k, v = bf16(rng, 30, heads, D), bf16(rng, 30, heads, D, gain=0.5)
+    dev = up(cache)
+    fq.kv_append_fp8(k, v, *dev, i32(table.tolist()), i32([0, 10, 20, 30]), i32([12, 31, 20]), 10)
+    want = fp8.kv_append(host(k), host(v), cache, table, [0, 10, 20, 30], [12, 31, 20])
+    for got, w in zip(dev, want):
+        assert np.array_equal(to_np(got), w)
+
+
 def test_append_reports_entries_out_of_range(fq):
     """Bad page ids, positions past the table and offsets past the tokens write nothing and are reported."""
     rng = np.random.default_rng(6)
