@@ -256,7 +256,7 @@ FP4Q_API fp4q_status fp4q_quantize_fp8(const void* x, int64_t M, int64_t K, int6
         p.n_items = spans(M, kFp8RowBlocks) * p.n_kb;
         if (p.n_items >= kMaxDim) return FP4Q_ERR_UNSUPPORTED;
         const int64_t per = kFp8RowThreads / 16;
-        const int grid = (int)std::min<int64_t>(spans(p.n_items, per), (int64_t)sms * 8);
+        const int grid = (int)std::min<int64_t>(spans(p.n_items, per), (int64_t)sms * 4);
         return launch(fp8_row_kernel, grid, kFp8RowThreads, 0, (cudaStream_t)stream, p);
     }
     p.n_items = spans(M, kFp8Block) * p.n_kb;

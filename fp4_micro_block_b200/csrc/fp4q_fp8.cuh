@@ -204,8 +204,20 @@ __global__ void __launch_bounds__(kFp8RowThreads) fp8_row_kernel(const Fp8QuantP
     for (int64_t base = first - half; base < p.n_items; base += step) {
         const int64_t c = (int64_t)kb * kFp8Block + l16 * 8, r0 = (int64_t)r4 * N;
         uint4 w[N];
+        const bool whole = r0 + N <= p.M && c + 8 <= p.K;
+        if (whole) {
+            const uint16_t* src = p.x + r0 * p.ldx + c;
 #pragma unroll
-        for (int k = 0; k < N; ++k) w[k] = fp8_load8(p, r0 + k, c);  // zeros past the last row
+            for (int k = 0; k < N; ++k) w[k] = __ldg(reinterpret_cast<const uint4*>(src + k * p.ldx));
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < N; ++k) {  // zeros past the last row and column
+                const uint4 x = fp8_load8(p, r0 + k, c);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (i == k) w[i] = x;
+            }
+        }
         uint32_t m[N / 2];
 #pragma unroll
         for (int k = 0; k < N / 2; ++k) {  // two rows' maxima in a word
@@ -217,12 +229,23 @@ __global__ void __launch_bounds__(kFp8RowThreads) fp8_row_kernel(const Fp8QuantP
         const uint32_t mine = (l16 & 2) ? m[1] : m[0];
         const Fp8Scale f = fp8_scale(fmaxf((l16 & 1) ? bf16hi(mine) : bf16lo(mine), 0.0f));
         if (l16 < N && r0 + l16 < p.M) p.scales[kb * p.lds + r0 + l16] = f.s;
+        uint8_t* dst = p.codes + r0 * p.ldc + c;
+        if (__all_sync(0xffffffffu, whole && f.nrz != 0.0f)) {  // no tests per block
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const Fp8Scale fk = fp8_scale_of(f, (lane & 16) + k);
-            const int64_t r = r0 + k;
-            if (r < p.M && c < p.K)
-                fp8_store8(p.codes + r * p.ldc + c, fp8_codes(w[k].x, w[k].y, fk), fp8_codes(w[k].z, w[k].w, fk), p.K - c);
+            for (int k = 0; k < N; ++k) {
+                const Fp8Scale fk = fp8_scale_of(f, (lane & 16) + k);
+                *reinterpret_cast<uint2*>(dst + k * p.ldc) = make_uint2(fp8_codes_fast(w[k].x, w[k].y, fk), fp8_codes_fast(w[k].z, w[k].w, fk));
+            }
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < N; ++k) {
+                const Fp8Scale fk = fp8_scale_of(f, (lane & 16) + k);
+                uint4 x = w[0];
+#pragma unroll
+                for (int i = 1; i < N; ++i)
+                    if (i == k) x = w[i];
+                if (r0 + k < p.M && c < p.K) fp8_store8(dst + k * p.ldc, fp8_codes(x.x, x.y, fk), fp8_codes(x.z, x.w, fk), p.K - c);
+            }
         }
         r4 += dr;
         kb += dkb;
