@@ -333,7 +333,18 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
 #pragma unroll 1
     for (int turn = warp; turn < turns; turn += kWarps) {
         if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * stage, phase))) {
-            if (lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
+            if (lane == 0) {
+                atomicOr(&g_device_error, kErrWaitTimeout);
+                // the turns on their way land before the ring is used again
+                for (int i = turn; i < turns && i < turn + S * kWarps; i += kWarps) {
+                    (void)mbar_wait(full0 + 8 * stage, phase);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            __syncwarp();
             break;
         }
         // The last turn may have one tile: what lies in the other's place is of

@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(640, 1)
         reg_dec<kTileRegsRoles>();
         if (warp == 0) {
             // -------------------------------------------- TMA: lane i < 8 brings keys 16 i .. of each tile
-            for (int j = 0; j < tiles; ++j) {
+            int j = 0;
+            for (; j < tiles; ++j) {
                 const int st = j & 1;
                 const int boxes = min(8, (most - j * kTileKeys + kAttnStep - 1) / kAttnStep);
                 const int32_t id = lane < boxes ? attn_page(p, b, (8 * j + lane) >> shift, true) : 0;
@@ -165,6 +166,8 @@ __global__ void __launch_bounds__(640, 1)
                 }
                 __syncwarp();
             }
+            // every copy lands before the CTA may exit
+            for (int i = j > 2 ? j - 2 : 0; i < j; ++i) (void)mbar_wait(full8 + 8 * (i & 1), (uint32_t)((i >> 1) & 1));
         } else if (warp == 1 && tiles > 0) {
             // -------------------------------------------- MMA: S runs two tiles ahead of P V
             // The whole warp goes through the loop, so that addresses stay in uniform

@@ -271,6 +271,7 @@ constexpr int kFp8TurnedOff = kFp8TileStages * kFp8TileBytes;
 constexpr int kFp8PartOff = kFp8TurnedOff + kFp8Block * kFp8Block;
 constexpr int kFp8ColOff = kFp8PartOff + 8 * (kFp8Block / 2) * 4;
 constexpr int kFp8TileBarOff = kFp8ColOff + kFp8Block * 16;
+static_assert(kFp8TileStages == 2, "this tile and the next one");
 constexpr int kFp8TileSmem = 1024 + kFp8TileBarOff + 8 * kFp8TileStages;
 constexpr int kFp8TileCtas = 2;  // per SM
 
@@ -308,7 +309,13 @@ __global__ void __launch_bounds__(kFp8TileThreads, kFp8TileCtas)
     uint32_t phase = 0;
     for (uint32_t item = blockIdx.x; item < n_items; item += gridDim.x) {
         if (!__syncthreads_and(mbar_wait(full0 + 8 * stage, phase))) {
-            if (tid == 0) atomicOr(&g_device_error, kErrWaitTimeout);
+            if (tid == 0) {
+                atomicOr(&g_device_error, kErrWaitTimeout);
+                // the copies on their way land before the CTA exits: this tile's, and the next one's
+                (void)mbar_wait(full0 + 8 * stage, phase);
+                if (item + gridDim.x < n_items) (void)mbar_wait(full0 + 8 * (stage ^ 1), phase ^ (uint32_t)stage);
+            }
+            __syncthreads();
             return;
         }
         const uint32_t mb = item / n_kb, kb = item - mb * n_kb;

@@ -17,8 +17,10 @@
 //                  are added through distributed shared memory in rank order.
 //
 // CTA roles: warp 0 lane 0 streams the K blocks of both operands by TMA into a
-// ring; warp 1 allocates TMEM, lane 0 issues the MMAs; the other warps (one
-// group of four per 128 columns) scale and accumulate, then store.
+// ring; warp 1 allocates TMEM and issues the MMAs (as a whole, one lane elected:
+// a branch on lane 0 kept the descriptors out of uniform registers, 158 us
+// against 141 for 8192x4096x4096); the other warps (groups of four, each with
+// its columns) scale and accumulate, then store.
 // Every wait is bounded; a wait that runs out sets g_device_error and the role
 // stops; the CTA drains its copies and MMAs and frees TMEM before it exits.
 #pragma once
