@@ -336,6 +336,8 @@ def fp4q_quantize_fp8(x, block, codes=None, scales=None, codes_t=None, scales_t=
     """E4M3 codes and block-128 scales of bf16 x [M, K] and / or of its transpose."""
     _want(x, "x", _BF16, None, None)
     M, K = x.shape
+    if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
+        raise ValueError("fp4q_quantize_fp8: codes and scales go together")
     dev = _device("fp4q_quantize_fp8", x, codes, scales, codes_t, scales_t)
     c = s = ct = st = None
     ldc = lds = ldct = ldst = 0

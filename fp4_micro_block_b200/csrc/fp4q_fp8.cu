@@ -438,7 +438,7 @@ FP4Q_API size_t fp4q_attention_fp8_workspace_bytes(int64_t batch, int64_t max_q,
                                                    int32_t num_kv_heads, int32_t head_dim) {
     const size_t bad = (size_t)-1;
     if (batch < 0 || max_q < 0 || max_len < 0 || num_kv_heads <= 0 || num_q_heads <= 0 ||
-        num_q_heads % num_kv_heads != 0 || head_dim <= 0 || batch >= kMaxDim || max_q >= kMaxDim || max_len >= kMaxDim)
+        num_q_heads % num_kv_heads != 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256) || batch >= kMaxDim || max_q >= kMaxDim || max_len >= kMaxDim)
         return bad;
     if (batch == 0 || max_q == 0) return 0;
     int sms = 0;

@@ -345,7 +345,9 @@ fp4q_status fp4q_quantize_fp8(const void* x, int64_t M, int64_t K, int64_t ldx, 
 /* fp4q_gemm_fp8 -- block-scaled FP8 GEMM on the tensor cores,
  *   D[m, n] = sum over blocks kb of SA[kb, m] * SB[kb, n] *
  *             sum over k in kb of E4M3(A[m, k]) * E4M3(B[n, k])
- * with FP32 sums.
+ * with FP32 sums.  A block's sum is multiplied by the two scales one after the
+ * other or by their product, in FP32: where a step leaves FP32's normal range (a
+ * scale near 1e31, a product of scales below 1e-38) the result is inf or loses bits.
  *   a_codes   uint8 [M, lda], a_scales float [ceil(K/128), ldas] (FP4Q_FP8_ROW).
  *   b_codes   uint8 [N, ldb], b_scales float [ceil(K/128), ldbs], of FP4Q_FP8_ROW
  *             or FP4Q_FP8_TILE blocks (b_block).

@@ -132,3 +132,17 @@ def test_binding_refuses_host_tensors_wrong_types_and_shapes(fq):
     assert fq._tokens(torch.zeros((5, 8, 64), dtype=torch.bfloat16)[:, 2:4], "q", 5, 2, 64) == 512
     c = fq.Fp4qKvCache(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
     assert bytes(c) == fq._KV.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
+
+
+def test_workspace_query_refuses_the_head_dims_that_the_call_refuses(fq):
+    w = fq.lib().fp4q_attention_fp8_workspace_bytes
+    for dim in (1, 32, 96, 512):
+        assert w(1, 1, 1, 4, 2, dim) == C.c_size_t(-1).value
+
+
+def test_binding_refuses_codes_without_scales(fq):
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    codes, scales = fq.alloc_fp8(4, 64, device="cpu")
+    for out in ((codes, None), (None, scales), (codes, scales, codes, None), (codes, scales, None, scales)):
+        with pytest.raises(ValueError, match="together"):
+            fq.fp4q_quantize_fp8(x, fq.FP4Q_FP8_ROW, *out)
