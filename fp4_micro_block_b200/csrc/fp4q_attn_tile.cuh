@@ -40,7 +40,8 @@ struct AttnTileGeo {
     static constexpr int ml_off = mref_off + 4 * kTileRows * 4;     // [2][2][128]: maxima, denominators
     static constexpr int qs_off = ml_off + 4 * kTileRows * 4;       // [128]: the queries' scales
     static constexpr int nan_off = qs_off + kTileRows * 4;      // [D]: first key with a NaN in V's column
-    static constexpr int bar_off = nan_off + D * 4;
+    static constexpr int sc_off = nan_off + D * 4;              // [8][8]: scales of the tiles' runs of 16 keys
+    static constexpr int bar_off = sc_off + 8 * 8 * 16;
     static constexpr int num_bars = 21;
     static constexpr int slot_off = bar_off + 8 * num_bars;
     static constexpr int smem = 1024 + slot_off + 16;
@@ -97,12 +98,13 @@ __global__ void __launch_bounds__(640, 1)
     float* q_scale = reinterpret_cast<float*>(smem + G::qs_off);
     float* ml = reinterpret_cast<float*>(smem + G::ml_off);
     int* nan_key = reinterpret_cast<int*>(smem + G::nan_off);
+    float4(*run_scale)[8] = reinterpret_cast<float4(*)[8]>(smem + G::sc_off);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::slot_off);
     if (tid == 0) {
         prefetch_tmap(&map_k);
         prefetch_tmap(&map_v);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(full8 + 8 * i, 1);
+            mbar_init(full8 + 8 * i, 2);
             mbar_init(empty8 + 8 * i, 4);
             mbar_init(kfull + 8 * i, 4);
             mbar_init(kfree + 8 * i, 1);
@@ -147,11 +149,22 @@ __global__ void __launch_bounds__(640, 1)
         reg_dec<kTileRegsRoles>();
         if (warp == 0) {
             // -------------------------------------------- TMA: lane i < 8 brings keys 16 i .. of each tile
+            // It also leaves the scales of these runs in shared memory, eight tiles deep
+            // (the copies are at most six tiles ahead of the softmax): the softmax warps
+            // would stall on a page's id and then on its scale (two chunks of 1000 over
+            // 4096 keys: 181 us so, 174 with this).
             int j = 0;
+            int32_t next = lane < 8 && lane * kAttnStep < most ? attn_page(p, b, lane >> shift, true) : 0;
             for (; j < tiles; ++j) {
                 const int st = j & 1;
                 const int boxes = min(8, (most - j * kTileKeys + kAttnStep - 1) / kAttnStep);
-                const int32_t id = lane < boxes ? attn_page(p, b, (8 * j + lane) >> shift, true) : 0;
+                const int32_t id = next;
+                float ks = 0.0f, vs = 0.0f;
+                if (lane < boxes) {
+                    ks = __ldg(p.c.k_scale + (int64_t)id * p.c.heads + hk);
+                    vs = __ldg(p.c.v_scale + (int64_t)id * p.c.heads + hk);
+                }
+                if (lane < 8 && (j + 1) * kTileKeys + lane * kAttnStep < most) next = attn_page(p, b, (8 * (j + 1) + lane) >> shift, true);
                 if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait(empty8 + 8 * st, (uint32_t)(((j >> 1) - 1) & 1)))) {
                     if (lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
                     break;
@@ -164,7 +177,10 @@ __global__ void __launch_bounds__(640, 1)
                     tma_load_2d(dst, &map_k, 0, row, full8 + 8 * st);
                     tma_load_2d(dst + G::k8, &map_v, 0, row, full8 + 8 * st);
                 }
+                // (scales below 2^-100, and 0, weigh as 2^-100 in the maximum only)
+                if (lane < 8) run_scale[j & 7][lane] = make_float4(ks, vs * 0x1p14f, log2f(fmaxf(vs, 0x1p-100f)), 0.0f);
                 __syncwarp();
+                if (lane == 0) mbar_arrive(full8 + 8 * st);
             }
             // every copy lands before the CTA may exit
             for (int i = j > 2 ? j - 2 : 0; i < j; ++i) (void)mbar_wait(full8 + 8 * (i & 1), (uint32_t)((i >> 1) & 1));
@@ -257,23 +273,12 @@ __global__ void __launch_bounds__(640, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull);
         }
-        // lanes 0..7: the scales of the next tile's runs of 16 keys
-        float kn = 0.0f, vn = 0.0f;
-        auto scales = [&](int j) {
-            if (lane < 8 && j * kTileKeys + lane * kAttnStep < most) {
-                const int64_t at = attn_page(p, b, (8 * j + lane) >> shift, false) * (int64_t)p.c.heads + hk;
-                kn = __ldg(p.c.k_scale + at);
-                vn = __ldg(p.c.v_scale + at);
-            }
-        };
-        scales(odd);
         float m = -INFINITY, l = 0.0f;
         bool ok = __all_sync(0xffffffffu, mbar_wait(qfull, 0));
         const float qs = q_scale[t];
         for (int j = odd; j < tiles && ok; j += 2) {
             const int st = j & 1;
-            const float kv = kn, vv = vn, lv = log2f(fmaxf(vn, 0x1p-100f));
-            if (j + 2 < tiles) scales(j + 2);
+            const float4* sc = run_scale[j & 7];
             const int left = lim - j * kTileKeys;  // keys of the tile that this row sees
             const bool edge = (j + 1) * kTileKeys > every;
             ok = __all_sync(0xffffffffu, mbar_wait(sfull + 8 * st, (uint32_t)((j >> 1) & 1)));
@@ -300,9 +305,7 @@ __global__ void __launch_bounds__(640, 1)
                         mx[i] = fmaxf(fmaxf(__uint_as_float(x[16 * h + i]), __uint_as_float(x[16 * h + 4 + i])),
                                       fmaxf(__uint_as_float(x[16 * h + 8 + i]), __uint_as_float(x[16 * h + 12 + i])));
                     const int run = col / 16 + h;
-                    const float f = __shfl_sync(0xffffffffu, kv, run) * qs;
-                    top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f +
-                                         __shfl_sync(0xffffffffu, lv, run));  // (-inf * 0 is no number: skipped)
+                    top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), sc[run].x * qs, sc[run].z));  // (-inf * 0 is no number: skipped)
                 }
             }
             const float mn = fmaxf(m, top), a = mn == -INFINITY ? 1.0f : exp2_approx(m - mn), base = mn == -INFINITY ? 0.0f : mn;
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int run = col / 16 + h;
-                        const uint64_t f = f2_both(__shfl_sync(0xffffffffu, kv, run) * qs), wv = f2_both(__shfl_sync(0xffffffffu, vv, run) * 0x1p14f);
+                        const uint64_t f = f2_both(sc[run].x * qs), wv = f2_both(sc[run].y);
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             const uint64_t z = f2_fma(f2_pack(x[16 * h + i], x[16 * h + i + 1]), f, nb);
