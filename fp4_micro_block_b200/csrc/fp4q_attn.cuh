@@ -102,7 +102,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // read each other's slots in shared memory; the slots of more are in the
 // workspace, for a second kernel.
 template <int D>
-constexpr int kAttnSlot = D + 2;
+constexpr int kAttnSlot = D + 4;  // (whole 16-byte pieces)
 
 constexpr int kAttnRows = 16, kAttnStep = 16;
 constexpr int kAttnMaxChunk = 4096;   // keys of one split: its pages' ids and scales are in shared memory
@@ -110,7 +110,8 @@ constexpr int kAttnMaxChunk = 4096;   // keys of one split: its pages' ids and s
 struct AttnSplit {
     uint32_t row_tiles, splits;
     int32_t chunk;      // keys per split, a multiple of 128
-    uint32_t slot_rows; // rows of a tile that may exist: min(16, max_q * G)
+    uint32_t tile_rows; // kAttnRows or kTileRows
+    uint32_t slot_rows; // rows of a tile that may exist: min(tile_rows, max_q * G)
     float* ws;          // NULL: one split, or a cluster of them
 };
 
@@ -574,14 +575,14 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, cons
     const float* slots = sp.ws + (int64_t)u * sp.splits * kAttnSlot<D>;
     const uint32_t in_tile = u % sp.slot_rows;
     u /= sp.slot_rows;
-    const int row = (int)(u % sp.row_tiles * kAttnRows + in_tile);
+    const int row = (int)(u % sp.row_tiles * sp.tile_rows + in_tile);
     u /= sp.row_tiles;
     const int hk = (int)(u % (uint32_t)p.c.heads);
     const int64_t b = u / (uint32_t)p.c.heads;
     const AttnSeq s = attn_seq(p, b, false);
     if (row >= s.n * p.group) return;
     // the splits that its row tile filled (the first always)
-    const int last = min(s.n * p.group, (row / kAttnRows + 1) * kAttnRows) - 1;
+    const int last = min(s.n * p.group, (row / (int)sp.tile_rows + 1) * (int)sp.tile_rows) - 1;
     const int most = attn_limit(p, s, last);
     const int n = most > sp.chunk ? (most - 1) / sp.chunk + 1 : 1;
     float top = -INFINITY, l = 0.0f, v[D / 32];

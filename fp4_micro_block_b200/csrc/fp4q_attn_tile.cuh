@@ -82,10 +82,11 @@ __device__ __noinline__ void attn_note_nans(int* nan_key, uint32_t bytes, int ke
         if (bytes >> (8 * e) & 1u) atomicMin(nan_key + e, key);
 }
 
-template <int D>
+// SPLIT: a CTA has one run of the keys, and attn_join_kernel finishes the rows.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(640, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                     const AttnParams p, const uint32_t row_tiles) {
+                     const AttnParams p, const AttnSplit sp) {
     using G = AttnTileGeo<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = align_shared<1024>(smem_raw);
@@ -133,16 +134,21 @@ __global__ void __launch_bounds__(640, 1)
     const uint32_t tmem = *tmem_slot;
 
     uint32_t u = blockIdx.x;  // the last row tiles, which see most, first
-    const uint32_t rt = row_tiles - 1 - u % row_tiles;
-    u /= row_tiles;
+    const uint32_t split = SPLIT ? u % sp.splits : 0;
+    if (SPLIT) u /= sp.splits;
+    const uint32_t rt = sp.row_tiles - 1 - u % sp.row_tiles;
+    u /= sp.row_tiles;
     const int hk = (int)(u % (uint32_t)p.c.heads);
     const int64_t b = u / (uint32_t)p.c.heads;
     const AttnSeq s = attn_seq(p, b, tid == 0);
     const int r0 = (int)rt * kTileRows, n_rows = s.n * p.group;
     const int rows = min(n_rows - r0, kTileRows);
-    const int most = rows > 0 ? attn_limit(p, s, r0 + rows - 1) : 0;  // the last row sees most
+    // this split's keys k0 .. most - 1 of those that the tile sees (the last row sees most)
+    const int all = rows > 0 ? attn_limit(p, s, r0 + rows - 1) : 0;
+    const int k0 = SPLIT ? (int)min64((int64_t)split * sp.chunk, all) : 0, most = SPLIT ? min(all - k0, sp.chunk) + k0 : all;
     const int every = rows > 0 ? attn_limit(p, s, r0) : 0;            // keys below are seen by every row
-    const int tiles = (most + kTileKeys - 1) / kTileKeys;
+    const int tiles = (most - k0 + kTileKeys - 1) / kTileKeys;
+    const int run0 = k0 / kAttnStep;  // its first run of 16 keys
     const int per_page = p.c.page / kAttnStep, shift = per_page == 1 ? 0 : per_page == 2 ? 1 : per_page == 4 ? 2 : 3;
 
     if (wg == 0) {
@@ -154,17 +160,18 @@ __global__ void __launch_bounds__(640, 1)
             // would stall on a page's id and then on its scale (two chunks of 1000 over
             // 4096 keys: 181 us so, 174 with this).
             int j = 0;
-            int32_t next = lane < 8 && lane * kAttnStep < most ? attn_page(p, b, lane >> shift, true) : 0;
+            int32_t next = lane < 8 && k0 + lane * kAttnStep < most ? attn_page(p, b, (run0 + lane) >> shift, true) : 0;
             for (; j < tiles; ++j) {
                 const int st = j & 1;
-                const int boxes = min(8, (most - j * kTileKeys + kAttnStep - 1) / kAttnStep);
+                const int boxes = min(8, (most - k0 - j * kTileKeys + kAttnStep - 1) / kAttnStep);
                 const int32_t id = next;
                 float ks = 0.0f, vs = 0.0f;
                 if (lane < boxes) {
                     ks = __ldg(p.c.k_scale + (int64_t)id * p.c.heads + hk);
                     vs = __ldg(p.c.v_scale + (int64_t)id * p.c.heads + hk);
                 }
-                if (lane < 8 && (j + 1) * kTileKeys + lane * kAttnStep < most) next = attn_page(p, b, (8 * (j + 1) + lane) >> shift, true);
+                if (lane < 8 && k0 + (j + 1) * kTileKeys + lane * kAttnStep < most)
+                    next = attn_page(p, b, (run0 + 8 * (j + 1) + lane) >> shift, true);
                 if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait(empty8 + 8 * st, (uint32_t)(((j >> 1) - 1) & 1)))) {
                     if (lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
                     break;
@@ -279,8 +286,8 @@ __global__ void __launch_bounds__(640, 1)
         for (int j = odd; j < tiles && ok; j += 2) {
             const int st = j & 1;
             const float4* sc = run_scale[j & 7];
-            const int left = lim - j * kTileKeys;  // keys of the tile that this row sees
-            const bool edge = (j + 1) * kTileKeys > every;
+            const int left = lim - k0 - j * kTileKeys;  // keys of the tile that this row sees
+            const bool edge = k0 + (j + 1) * kTileKeys > every;
             ok = __all_sync(0xffffffffu, mbar_wait(sfull + 8 * st, (uint32_t)((j >> 1) & 1)));
             if (!ok) break;
             tc_fence_after();
@@ -385,15 +392,41 @@ __global__ void __launch_bounds__(640, 1)
         }
         ok = ok && __all_sync(0xffffffffu, mbar_wait(lfull, 0));
         if (!ok && lane == 0) atomicOr(&g_device_error, kErrWaitTimeout);
-        if (t < rows) {
-            float l = 0.0f;
+        float l = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float mk = ml[2 * k * kTileRows + t];
-                l = fmaf(ml[(2 * k + 1) * kTileRows + t], mk == -INFINITY ? 1.0f : exp2_approx(mk - mo), l);
+        for (int k = 0; k < 2; ++k) {
+            const float mk = ml[2 * k * kTileRows + t];
+            l = fmaf(ml[(2 * k + 1) * kTileRows + t], mk == -INFINITY ? 1.0f : exp2_approx(mk - mo), l);
+        }
+        const int lim = attn_limit(p, s, r);
+        if constexpr (SPLIT) {
+            // A warp's 32 rows through the K buffers, which no product reads any more, so
+            // that they leave in whole lines (64 queries over 4096 keys 20.8 us, 23.8 with
+            // each thread writing its own row).
+            if (ok && (split == 0 || tiles > 0)) {
+                constexpr int P = D / 4;  // 16-byte pieces of a row, swizzled by the row
+                float4* st = reinterpret_cast<float4*>(smem + G::kf_off) + (warp & 3) * 32 * P;
+#pragma unroll
+                for (int c = 0; c < P; ++c) {
+                    float v[4] = {f2_lo(o[2 * c]), f2_hi(o[2 * c]), f2_lo(o[2 * c + 1]), f2_hi(o[2 * c + 1])};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (nan_key[4 * c + i] < lim) v[i] = __int_as_float(0x7fffffff);
+                    st[lane * P + (c ^ (lane & 7))] = make_float4(v[0], v[1], v[2], v[3]);
+                }
+                __syncwarp();
+                const int w0 = t & ~31;  // the warp's first row
+                float* slots = sp.ws + (((int64_t)(b * p.c.heads + hk) * sp.row_tiles + rt) * sp.slot_rows * sp.splits + split) * kAttnSlot<D>;
+#pragma unroll 4
+                for (int i = lane; i < 32 * P; i += 32) {
+                    const int row = i / P, c = i % P;
+                    if (w0 + row < rows)
+                        *reinterpret_cast<float4*>(slots + (int64_t)(w0 + row) * sp.splits * kAttnSlot<D> + 4 * c) = st[row * P + (c ^ (row & 7))];
+                }
+                if (t < rows) *reinterpret_cast<float2*>(slots + (int64_t)t * sp.splits * kAttnSlot<D> + D) = make_float2(mo, l);
             }
+        } else if (t < rows) {
             const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
-            const int lim = attn_limit(p, s, r);
             const uint32_t tok = (uint32_t)r / (uint32_t)p.group, h = hk * p.group + (r - tok * p.group);
             uint4* dst = reinterpret_cast<uint4*>(p.o + (s.first + tok) * p.ldo + (int64_t)h * D);
 #pragma unroll
@@ -401,8 +434,8 @@ __global__ void __launch_bounds__(640, 1)
                 float v[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    v[2 * i] = __uint_as_float((uint32_t)o[4 * c + i]) * inv;
-                    v[2 * i + 1] = __uint_as_float((uint32_t)(o[4 * c + i] >> 32)) * inv;
+                    v[2 * i] = f2_lo(o[4 * c + i]) * inv;
+                    v[2 * i + 1] = f2_hi(o[4 * c + i]) * inv;
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -427,7 +460,7 @@ __global__ void __launch_bounds__(640, 1)
         const int q = (t & 3) | (t >> 5) << 2, w0 = (t >> 2) & 7;
         bool ok = true;
         for (int j = 0; j < tiles; ++j) {
-            const int st = j & 1, key0 = j * kTileKeys;
+            const int st = j & 1, key0 = k0 + j * kTileKeys;
             const uint32_t ph = (uint32_t)((j >> 1) & 1);
             ok = mbar_wait(full8 + 8 * st, ph) && (j < 2 || mbar_wait(kfree + 8 * st, ph ^ 1u));
             ok = __all_sync(0xffffffffu, ok);

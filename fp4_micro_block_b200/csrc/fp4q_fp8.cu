@@ -337,24 +337,36 @@ namespace {
 struct AttnPlan {
     bool tile;     // attn_tile_kernel
     bool cluster;  // the splits of a row tile join within a cluster
-    int64_t row_tiles, splits, chunk, slot_rows;
+    int64_t tile_rows, row_tiles, splits, chunk, slot_rows;
     size_t ws_bytes;
 };
 
 constexpr int64_t kAttnMost = (int64_t)1 << 30;
 constexpr int64_t kAttnCluster = 8;
 
+// Keys of one split of attn_tile_kernel: as many splits as fill the GPU, of 512
+// keys at least (a tile of 128 keys takes 1.45 us, the join 4 us and more).
+int64_t attn_tile_chunk(int64_t items, int64_t max_len, int sms) {
+    const int64_t want = std::max<int64_t>(1, sms / items);
+    return std::max<int64_t>(512, spans(spans(max_len, want), kTileKeys) * kTileKeys);
+}
+
 // Whether attn_tile_kernel (128 rows a CTA) is the faster one, by what it and
-// attn_rows_kernel (16 rows) took on one B200 at D = 128, in ns: 7000 and 1550 a
-// wave and 128 keys against 6000, 18 a key for each of the 3 CTAs an SM holds,
-// and 64 a row tile for the join where the keys are split.  Measured, in us (tile
-// / rows), 8 K/V heads of 4: 32 queries over 512 keys 13.9 / 13.1, 64 over 512
-// 14.0 / 19.7, 64 over 4096 53.6 / 41.6, 128 over 4096 53.8 / 64.1, two of 400
-// over 4096 95 / 208; 16 sequences of 8 queries in groups of 8 over 2000 31 / 47.
+// attn_rows_kernel (16 rows) took on one B200 at D = 128, in ns: 7000 and 1450 a
+// wave and 128 keys, with 4000 and 0.35 a row of a slot where the keys are split,
+// against 6000, 18 a key for each of the 3 CTAs an SM holds, and 64 a row tile for
+// the join.  Measured, in us (tile / rows), 8 K/V heads of 4: 32 queries over 512
+// keys 13.6 / 13.1, 64 over 512 13.7 / 19.9, 16 over 4096 17.5 / 17.2, 32 over 4096
+// 19.5 / 25.9, 64 over 4096 20.8 / 40.2 (keys not split 51.7), 128 over 4096 30.0 /
+// 62.8 (51.8), two of 100 over 4096 44.0 / 77.1 (51.9), two of 400 92 / 207; one K/V
+// head, 64 over 4096 16.9 / 14.5; 16 sequences of 8 queries in groups of 8 over 2000
+// 29.8 / 46.4.
 bool attn_take_tile(int64_t row_items, int64_t tile_items, int64_t max_len, int64_t rows, int sms) {
     if (rows <= kAttnRows) return false;
     const double by_rows = 6000.0 + 18.0 * row_items * max_len / (3.0 * sms) + (row_items < 3 * (int64_t)sms ? 64.0 * row_items : 0.0);
-    const double by_tile = 7000.0 + 1550.0 * spans(tile_items, sms) * spans(max_len, kTileKeys);
+    const int64_t chunk = attn_tile_chunk(tile_items, max_len, sms), splits = std::max<int64_t>(1, spans(max_len, chunk));
+    const double by_tile = 7000.0 + 1450.0 * spans(tile_items * splits, sms) * spans(std::min(max_len, chunk), kTileKeys) +
+                           (splits > 1 ? 4000.0 + 0.35 * tile_items * splits * std::min<int64_t>(rows, kTileRows) : 0.0);
     return by_tile < by_rows;
 }
 
@@ -365,25 +377,25 @@ fp4q_status attn_plan(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_h
     if (max_len > kAttnMost || max_q > kAttnMost / (q_heads / kv_heads)) return FP4Q_ERR_UNSUPPORTED;
     const int64_t rows = max_q * (q_heads / kv_heads), heads = batch * kv_heads;
     a.tile = dim <= 128 && attn_take_tile(heads * spans(rows, kAttnRows), heads * spans(rows, kTileRows), max_len, rows, sms);
-    a.row_tiles = spans(rows, a.tile ? kTileRows : kAttnRows);
+    a.tile_rows = a.tile ? kTileRows : kAttnRows;
+    a.row_tiles = spans(rows, a.tile_rows);
+    a.slot_rows = std::min<int64_t>(a.tile_rows, rows);
     if (a.row_tiles >= kMaxDim / kv_heads || a.row_tiles * kv_heads >= kMaxDim / batch) return FP4Q_ERR_UNSUPPORTED;
-    if (a.tile) {
-        *out = a;
-        return FP4Q_OK;
-    }
-    a.slot_rows = std::min<int64_t>(kAttnRows, max_q * (q_heads / kv_heads));
     const int64_t items = batch * kv_heads * a.row_tiles;
-    // three CTAs fit on an SM
-    const int64_t want = std::max<int64_t>(1, spans(3 * (int64_t)sms, items));
-    a.chunk = std::min<int64_t>(kAttnMaxChunk, std::max<int64_t>(128, spans(spans(max_len, want), 128) * 128));
+    if (a.tile) {
+        a.chunk = attn_tile_chunk(items, max_len, sms);
+    } else {  // three CTAs fit on an SM
+        const int64_t want = std::max<int64_t>(1, spans(3 * (int64_t)sms, items));
+        a.chunk = std::min<int64_t>(kAttnMaxChunk, std::max<int64_t>(128, spans(spans(max_len, want), 128) * 128));
+    }
     a.splits = std::max<int64_t>(1, spans(max_len, a.chunk));
     // A cluster saves the second launch (4 us of the host's time, none of the GPU's)
     // but holds its CTAs until the last is done: 32 x 8192 keys in clusters of two
     // took 111 us, with the second kernel 85.  So only where all have an SM to
     // themselves.
-    a.cluster = a.splits > 1 && a.splits <= kAttnCluster && items * a.splits <= sms;
-    if (a.splits >= kMaxDim / items || items >= kMaxDim / kAttnRows) return FP4Q_ERR_UNSUPPORTED;
-    a.ws_bytes = a.splits > 1 && !a.cluster ? (size_t)(items * a.splits * a.slot_rows * (dim + 2)) * sizeof(float) : 0;
+    a.cluster = !a.tile && a.splits > 1 && a.splits <= kAttnCluster && items * a.splits <= sms;
+    if (a.splits >= kMaxDim / items || items >= kMaxDim / a.tile_rows) return FP4Q_ERR_UNSUPPORTED;
+    a.ws_bytes = a.splits > 1 && !a.cluster ? (size_t)(items * a.splits * a.slot_rows * (dim + 4)) * sizeof(float) : 0;
     *out = a;
     return FP4Q_OK;
 }
@@ -404,22 +416,31 @@ fp4q_status make_kv_map(CUtensorMap* map, const KvCacheView& c, const uint8_t* c
     return r == CUDA_SUCCESS ? FP4Q_OK : FP4Q_ERR_CUDA;
 }
 
-template <int D>
-fp4q_status launch_attn_tile(const AttnParams& p, const AttnPlan& a, cudaStream_t s) {
+AttnSplit attn_split(const AttnPlan& a, void* ws) {
+    return {(uint32_t)a.row_tiles, (uint32_t)a.splits, (int32_t)a.chunk, (uint32_t)a.tile_rows, (uint32_t)a.slot_rows,
+            a.ws_bytes > 0 ? static_cast<float*>(ws) : nullptr};
+}
+
+template <int D, bool SPLIT>
+fp4q_status launch_attn_tile(const AttnParams& p, const AttnPlan& a, void* ws, cudaStream_t s) {
     using G = AttnTileGeo<D>;
-    auto kern = attn_tile_kernel<D>;
+    const AttnSplit sp = attn_split(a, ws);
+    auto kern = attn_tile_kernel<D, SPLIT>;
     static std::atomic<uint64_t> done{0};
     fp4q_status st = ensure_smem(kern, G::smem, done);
     if (st != FP4Q_OK) return st;
     CUtensorMap map_k, map_v;
     if ((st = make_kv_map(&map_k, p.c, p.c.k)) != FP4Q_OK || (st = make_kv_map(&map_v, p.c, p.c.v)) != FP4Q_OK) return st;
-    return launch(kern, (int)(p.batch * p.c.heads * a.row_tiles), G::threads, G::smem, s, map_k, map_v, p, (uint32_t)a.row_tiles);
+    const int64_t items = p.batch * p.c.heads * a.row_tiles;
+    st = launch(kern, (int)(items * a.splits), G::threads, G::smem, s, map_k, map_v, p, sp);
+    if (st != FP4Q_OK || a.ws_bytes == 0) return st;
+    return launch(attn_join_kernel<D>, (int)(items * a.slot_rows), 128, 0, s, p, sp);
 }
 
 template <int D>
 fp4q_status launch_attn(const AttnParams& p, const AttnPlan& a, void* ws, cudaStream_t s) {
     using G = AttnGeo<D>;
-    AttnSplit sp{(uint32_t)a.row_tiles, (uint32_t)a.splits, (int32_t)a.chunk, (uint32_t)a.slot_rows, a.ws_bytes > 0 ? static_cast<float*>(ws) : nullptr};
+    const AttnSplit sp = attn_split(a, ws);
     auto kern = attn_rows_kernel<D>;
     static std::atomic<uint64_t> done{0};
     fp4q_status st = ensure_smem(kern, G::smem, done);
@@ -495,7 +516,8 @@ FP4Q_API fp4q_status fp4q_attention_fp8(const void* q, int64_t ldq, int64_t toke
         if (!aligned(workspace, 16)) return FP4Q_ERR_ALIGNMENT;
     }
     if (a.tile)
-        return p.c.dim == 64 ? launch_attn_tile<64>(p, a, (cudaStream_t)stream) : launch_attn_tile<128>(p, a, (cudaStream_t)stream);
+        return a.splits > 1 ? (p.c.dim == 64 ? launch_attn_tile<64, true> : launch_attn_tile<128, true>)(p, a, workspace, (cudaStream_t)stream)
+                            : (p.c.dim == 64 ? launch_attn_tile<64, false> : launch_attn_tile<128, false>)(p, a, workspace, (cudaStream_t)stream);
     if (p.c.dim == 64) return launch_attn<64>(p, a, workspace, (cudaStream_t)stream);
     if (p.c.dim == 128) return launch_attn<128>(p, a, workspace, (cudaStream_t)stream);
     return launch_attn<256>(p, a, workspace, (cudaStream_t)stream);

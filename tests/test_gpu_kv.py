@@ -633,3 +633,60 @@ def test_offsets_past_32_bits(fq, new, B):
     for a, b in zip(small, big):
         assert torch.equal(a, b[shift:])
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (64, 128), (128, 16), (128, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_chunks_over_long_sequences(fq, D, page, causal):
+    """Few tiles of 128 rows over many keys: the keys are split and joined through the workspace."""
+    rng = np.random.default_rng(D + page + causal)
+    # splits that a sequence does not reach; more queries than keys
+    for heads, new, lens in ((3, [100, 3, 0, 130, 70], [2500, 700, 60, 130, 30]), (2, [100, 3, 0, 70], [2500, 700, 60, 30])):
+        n = fq.fp4q_attention_fp8_workspace_bytes(len(new), max(new), max(lens), 4 * heads, heads, D)
+        ws = torch.full((n + 16,), 255, dtype=torch.uint8, device="cuda")  # every word of it a NaN
+        run(fq, rng, new, lens, page, D, heads, 4, causal, ws=ws)
+    assert n > 0
+
+
+@pytest.mark.parametrize("L", [511, 512, 513, 640, 1024, 1025, 1537])
+def test_chunks_around_the_splits_ends(fq, L):
+    rng = np.random.default_rng(L)
+    run(fq, rng, [128], [L], 32, 128, 1, 8)
+    run(fq, rng, [128, 60], [L, 513], 64, 64, 2, 4, causal=False)
+
+
+def test_chunks_over_long_sequences_with_a_nan(fq):
+    """A NaN code of V reaches the rows that see its key, whichever split it is in."""
+    rng = np.random.default_rng(41)
+    page, D, L, new, heads, G = 64, 128, 2000, 128, 2, 4
+    cache, table, cu, q = batch_of(fq, rng, 1, new, L, page, D, heads, G)
+    at = [700, L - 30]  # seen by all, and by the last queries only
+    for d, pos in enumerate(at):
+        cache[1][table[0, pos // page], 0, pos % page, 5 + d] = 0x7F
+    o, _ = fq.attention_fp8(q, *up(cache), i32(table.tolist()), i32(cu), i32([L]), new, L)
+    bad = np.isnan(to_np(o.float()))
+    want = np.zeros_like(bad)
+    want[:, :G, 5] = True
+    want[new - 30:, :G, 6] = True  # key L - 30 is query new - 30's own
+    assert np.array_equal(bad, want)
+
+
+def test_chunks_over_long_sequences_in_a_graph(fq):
+    """Lengths that change between replays, below the bound that the splits were made for."""
+    rng = np.random.default_rng(42)
+    page, D, L, new, heads, G = 64, 128, 3000, 100, 2, 4
+    cache, table, cu, q = batch_of(fq, rng, 2, new, L, page, D, heads, G)
+    dev, tab, dcu, lens = up(cache), i32(table.tolist()), i32(cu), i32([L, L])
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ws = fq.attention_fp8_workspace(q, dev[0], 2, new, L)
+    call = lambda: fq.fp4q_attention_fp8(q, *dev, tab, dcu, lens, new, L, o, lse, workspace=ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for ns in ([3000, 40], [600, 2999], [0, 513]):
+        lens.copy_(i32(ns))
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(o, lse, q, cache, table, cu, ns, True, D ** -0.5)
