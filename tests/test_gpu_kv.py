@@ -690,3 +690,13 @@ def test_chunks_over_long_sequences_in_a_graph(fq):
         graph.replay()
         torch.cuda.synchronize()
         compare(o, lse, q, cache, table, cu, ns, True, D ** -0.5)
+
+
+def test_the_largest_bounds(fq):
+    """max_q * G and max_len up to 2^30 are taken, whatever the heads; more is refused."""
+    most = 1 << 30
+    assert fq.fp4q_attention_fp8_workspace_bytes(2, most, 64, 8, 8, 128) == 0
+    assert fq.fp4q_attention_fp8_workspace_bytes(2, most // 4, 64, 32, 8, 64) == 0
+    for sizes in ((1, most + 1, 64, 8, 8, 128), (1, most // 4 + 1, 64, 32, 8, 128), (1, 1, most + 1, 8, 8, 128)):
+        with pytest.raises(fq.Fp4qError):
+            fq.fp4q_attention_fp8_workspace_bytes(*sizes)
