@@ -593,9 +593,8 @@ def attention_fp8_workspace(q, k_cache, batch, max_q, max_len):
 def attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, max_q, max_len, causal=True,
                   softmax_scale=None, ws=None):
     """(o [tokens, Hq, D] bf16, lse [tokens, Hq] f32); tokens that belong to no sequence are left unset."""
-    T, Hq, D = q.shape
-    o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)  # (1.4 us of the host; torch.empty 2.4)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     if ws is None:
         ws = attention_fp8_workspace(q, k_cache, block_table.shape[0], max_q, max_len)
     fp4q_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, max_q, max_len, o, lse, causal,
