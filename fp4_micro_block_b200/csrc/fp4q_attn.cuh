@@ -77,8 +77,8 @@ __device__ __forceinline__ int32_t attn_page(const AttnParams& p, int64_t b, int
 // in fp16: full precision whatever the V scales are, and down to 2^-28 of the
 // largest before fp16's subnormals.  The denominator sums w / vs in fp32.
 //
-// 32 tokens over 6000 keys on average, 8 K/V heads of 128 in groups of 4: 85 us,
-// 0.71 of the copy rate (the codes' conversion keeps the ALU at 42 %); one token
+// 32 tokens over 6000 keys on average, 8 K/V heads of 128 in groups of 4: 76 us,
+// 0.80 of the copy rate (the codes' conversion keeps the ALU at 42 %); one token
 // over 500 7.5 us, the latency of its steps.
 
 constexpr float kAttnWeightLog2 = 14.0f;
@@ -242,8 +242,19 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
     pdl_wait();
     pdl_trigger();
     uint32_t u = blockIdx.x;  // (32-bit divisions: each 64-bit one here costs a tenth of a microsecond)
-    const uint32_t split = u % sp.splits;
-    u /= sp.splits;
+    const bool joined = sp.splits > 1 && !sp.ws;  // a cluster: every CTA of it stays to the end
+    uint32_t split;
+    if (joined) {
+        split = u % sp.splits;
+        u /= sp.splits;
+    } else {
+        // The first splits, most of them full, go first, and the later ones, of which
+        // less is left, fill in behind them (32 tokens over 2048 to 8192 keys: 76 us;
+        // a row tile's splits one after the other 86; 8 over 500 to 2000: 16.0 / 15.6).
+        const uint32_t items = gridDim.x / sp.splits;
+        split = u / items;
+        u -= split * items;
+    }
     const uint32_t rt = u % sp.row_tiles;
     u /= sp.row_tiles;
     const int hk = (int)(u % (uint32_t)p.c.heads);
@@ -255,7 +266,6 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
     // keys this tile sees (the last row sees most), and this split's part of them
     const int most = attn_limit(p, s, r0 + rows - 1);
     const int k0 = (int)min64((int64_t)split * sp.chunk, most), k1 = min(most - k0, sp.chunk) + k0;
-    const bool joined = sp.splits > 1 && !sp.ws;  // a cluster: every CTA of it stays to the end
     if (split > 0 && k0 >= k1 && !joined) return;
     const int every = attn_limit(p, s, r0);  // keys below are seen by every row of the tile
     const int lim0 = attn_limit(p, s, r0 + g), lim1 = attn_limit(p, s, r0 + g + 8);
