@@ -104,8 +104,12 @@ __device__ __forceinline__ Fp8Scale fp8_scale_of(const Fp8Scale& f, int src) {
     r.nlo = __shfl_sync(0xffffffffu, f.nlo, src);
     return r;
 }
+// s == 0: the block has zeros and NaN alone, which give the codes 0 and 0x7f.
 __device__ __noinline__ uint32_t fp8_codes_ieee(uint32_t u0, uint32_t u1, float s) {
-    if (s == 0.0f) return 0u;
+    if (s == 0.0f) {
+        auto code = [](float v) { return fabsf(v) * 0.0f; };
+        return e4m3_pack4(code(bf16lo(u0)), code(bf16hi(u0)), code(bf16lo(u1)), code(bf16hi(u1)));
+    }
     return e4m3_pack4(__fdiv_rn(bf16lo(u0), s), __fdiv_rn(bf16hi(u0), s), __fdiv_rn(bf16lo(u1), s), __fdiv_rn(bf16hi(u1), s));
 }
 // The four codes of two words of bf16 pairs: x / s as div_split computes it,

@@ -309,8 +309,10 @@ fp4q_status fp4q_dequantize_signed(fp4q_format format, const uint8_t* codes, con
  *  - E4M3 rounding: nearest value, ties to the even code, saturating at +-448,
  *    sign kept; a NaN gives the NaN code 0x7f.
  *  - Blocks: s = amax/448 (IEEE binary32 division), code = E4M3(x/s) with x/s
- *    correctly rounded; s == 0 gives zero codes.  The maximum skips NaN; a block
- *    that holds an infinity has s = inf and dequantizes to NaN.
+ *    correctly rounded.  The maximum skips NaN: a block without a number other
+ *    than 0 has s = 0, code 0 for its zeros and 0x7f for its NaN (0x7f under a
+ *    scale of 0 is NaN).  A block that holds an infinity has s = inf and
+ *    dequantizes to NaN.
  *  - Cache pages: the scale is the smallest power of two s >= amax/448 (at
  *    least 2^-126; 0 for a page of zeros), so a page whose scale grows moves
  *    its codes by an exact power of two (rounded again only where they become

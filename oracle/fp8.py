@@ -41,8 +41,10 @@ def _amax(v, axis):
 
 
 def _quot(x, s):
+    """x / s in binary32; where s is 0, x holds zeros and NaN alone: 0 and NaN."""
     with np.errstate(all="ignore"):
-        return np.where(s == 0, np.float32(0), x / np.where(s == 0, np.float32(1), s)).astype(np.float32)
+        none = np.where(np.isnan(x), np.float32(np.nan), np.float32(0))
+        return np.where(s == 0, none, x / np.where(s == 0, np.float32(1), s)).astype(np.float32)
 
 
 def quantize(x: np.ndarray, tile: bool):

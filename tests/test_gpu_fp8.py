@@ -291,3 +291,43 @@ def test_offsets_past_32_bits(fq):
     w = fq.quantize_fp8(activations(N, K, 52), fq.FP4Q_FP8_TILE)
     D = fq.gemm_fp8(*a, *w)
     assert D.numel() > 2 ** 31 and torch.equal(D[-last:], fq.gemm_fp8(*alone, *w))
+
+
+# ------------------------------------------------------------------ NaN in blocks without numbers
+
+@pytest.mark.parametrize("block", ["row", "tile"])
+@pytest.mark.parametrize("shape", [(1, 128), (3, 200), (130, 300)])
+def test_quantize_keeps_nans_of_blocks_without_numbers(fq, shape, block):
+    """A row, a tile and a column that are NaN throughout, and NaN among zeros: the NaN code wherever x is NaN."""
+    M, K = shape
+    x = activations(M, -(-K // 8) * 8, 61)[:, :K]
+    x[0] = float("nan")
+    if M > 2:
+        x[:, 128:] = 0.0
+        x[1, 130] = float("nan")
+        x[2] = -0.0
+        x[2, K - 1] = float("nan")
+        x[:, 7] = float("nan")
+    if M > 128:
+        x[:128, :128] = float("nan")
+    tile = block == "tile"
+    got = fq.quantize_fp8(x, fq.FP4Q_FP8_TILE if tile else fq.FP4Q_FP8_ROW, True)
+    alone = fq.quantize_fp8(x, fq.FP4Q_FP8_TILE if tile else fq.FP4Q_FP8_ROW)
+    assert torch.equal(alone[0], got[0]) and torch.equal(alone[1], got[1])
+    for (c, s), v in ((got[:2], host(x)), (got[2:], np.ascontiguousarray(host(x).T))):
+        want, want_s = fp8.quantize(v, tile)
+        assert np.array_equal(to_np(s), want_s) and np.array_equal(to_np(c) == 0x7F, np.isnan(v))
+        assert np.array_equal(to_np(c), want)
+
+
+@pytest.mark.parametrize("M", [1, 5, 200])
+def test_gemm_of_a_row_that_is_all_nan(fq, M):
+    """The row's products are NaN, not zeros, and the others' are as without it."""
+    N, K = 300, 392
+    x = activations(M, K, 63)
+    w = fq.quantize_fp8(activations(N, K, 64), fq.FP4Q_FP8_TILE)
+    clean = fq.gemm_fp8(*fq.quantize_fp8(x), *w)
+    x[M // 2] = float("nan")
+    D = fq.gemm_fp8(*fq.quantize_fp8(x), *w)
+    rest = [i for i in range(M) if i != M // 2]
+    assert torch.isnan(D[M // 2]).all() and torch.equal(D[rest], clean[rest])

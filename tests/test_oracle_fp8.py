@@ -76,3 +76,16 @@ def test_append_one_by_one_equals_at_once_but_for_subnormals():
         else:
             a, b = fp8.decode(once[i]), fp8.decode(many[i])
             assert (np.abs(a - b) <= np.where(np.abs(a) < 2.0 ** -5, 2.0 ** -9, 0)).all()
+
+
+@pytest.mark.parametrize("tile", [False, True])
+def test_a_nan_keeps_its_code_where_the_scale_is_zero(tile):
+    """A block without a number other than 0: scale 0, code 0 for the zeros of both signs, the NaN code for NaN."""
+    x = np.zeros((130, 200), np.float32)
+    x[0] = np.nan
+    x[1, 5] = np.nan
+    x[2] = -0.0
+    x[129, 199] = np.nan
+    codes, scales = fp8.quantize(x, tile)
+    assert not scales.any() and np.array_equal(codes, np.where(np.isnan(x), 0x7F, 0))
+    assert np.array_equal(np.isnan(fp8.values(codes, scales, tile)), np.isnan(x))
