@@ -107,19 +107,21 @@ __global__ void __launch_bounds__(kKvMaxThreads) kv_append_kernel(const KvAppend
     for (uint32_t k = 0; k < blockDim.x / 32; ++k) m = bf16x2_max(m, part[k]);
     const float s = fmaxf(old, kv_scale(bf16x2_top(m))), inv = kv_inverse(s);
     if (threadIdx.x == 0) *scale = s;
-    if (s > old && from > 0) {  // what the page has moves to the new scale (a page of zeros so far: zeros)
+    if (s > old && from > 0) {  // what the page has moves to the new scale (under a scale of 0: zeros and NaN, which stay)
         const float ratio = old * inv;
+        const uint32_t sign = old > 0.0f ? ~0u : 0x7fffffffu;  // (a zero of such a page has code 0)
         for (int e = threadIdx.x; e < from << p.per_row_log2; e += blockDim.x) {
             uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)e * 8);
             const uint2 x = *at;
             float f[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = e4m3_decode(((k < 4 ? x.x : x.y) >> (8 * (k & 3)))) * ratio;
-            *at = old > 0.0f ? make_uint2(e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7])) : make_uint2(0, 0);
+            for (int k = 0; k < 8; ++k)
+                f[k] = __uint_as_float(__float_as_uint(e4m3_decode(((k < 4 ? x.x : x.y) >> (8 * (k & 3)))) * ratio) & sign);
+            *at = make_uint2(e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7]));
         }
     }
     uint8_t* dst = codes + ((int64_t)from << (p.per_row_log2 + 3));
-    if ((__float_as_uint(s) & 0x7fffffu) == 0) {  // a power of two, as this kernel writes it: exact products
+    if (s != 0.0f && (__float_as_uint(s) & 0x7fffffu) == 0) {  // a power of two, as this kernel writes it: exact products
         const uint64_t inv2 = f2_both(inv);
 #pragma unroll
         for (int k = 0; k < kKvPieces; ++k) {
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kKvMaxThreads) kv_append_kernel(const KvAppend
                 make_uint2(e4m3_pack4(f2_lo(f[0]), f2_hi(f[0]), f2_lo(f[1]), f2_hi(f[1])),
                            e4m3_pack4(f2_lo(f[2]), f2_hi(f[2]), f2_lo(f[3]), f2_hi(f[3])));
         }
-    } else {  // a calibrated scale of the caller's
+    } else {  // a calibrated scale of the caller's, or a page without numbers
 #pragma unroll 1
         for (int e = threadIdx.x; e < count; e += blockDim.x) {
             const uint4 x = __ldg(reinterpret_cast<const uint4*>(rows + (e >> p.per_row_log2) * ld + (e & mask) * 8));

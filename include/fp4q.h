@@ -314,9 +314,10 @@ fp4q_status fp4q_dequantize_signed(fp4q_format format, const uint8_t* codes, con
  *    scale of 0 is NaN).  A block that holds an infinity has s = inf and
  *    dequantizes to NaN.
  *  - Cache pages: the scale is the smallest power of two s >= amax/448 (at
- *    least 2^-126; 0 for a page of zeros), so a page whose scale grows moves
- *    its codes by an exact power of two (rounded again only where they become
- *    E4M3 subnormals).
+ *    least 2^-126; 0 for a page without a number other than 0, whose codes are
+ *    as in such a block), so a page whose scale grows moves its codes by an
+ *    exact power of two (rounded again only where they become E4M3 subnormals).
+ *    NaN codes stay.
  * --------------------------------------------------------------------------- */
 typedef enum fp4q_fp8_block {
     FP4Q_FP8_ROW = 0, /* blocks of 1 row x 128 columns: scales [ceil(K/128), rows]             */

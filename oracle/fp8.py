@@ -104,7 +104,8 @@ def kv_append(k, v, cache, table, cu, lens):
                     old = scales[where, h] if kept else np.float32(0)
                     s = max(old, page_scale(_amax(new, None)))
                     if kept and s > old:
-                        codes[where, h, :kept] = encode(decode(codes[where, h, :kept]) * float(old) / float(s)) if old else 0
+                        x0 = decode(codes[where, h, :kept])
+                        codes[where, h, :kept] = encode(x0 * float(old) / float(s)) if old else encode(_quot(x0, old))
                     scales[where, h] = s
                     codes[where, h, kept:kept + hi - lo] = encode(_quot(new, np.float32(s)))
     return cache

@@ -700,3 +700,35 @@ def test_the_largest_bounds(fq):
     for sizes in ((1, most + 1, 64, 8, 8, 128), (1, most // 4 + 1, 64, 32, 8, 128), (1, 1, most + 1, 8, 8, 128)):
         with pytest.raises(fq.Fp4qError):
             fq.fp4q_attention_fp8_workspace_bytes(*sizes)
+
+
+# ------------------------------------------------------------------ NaN, infinities and scales at the ends of the range
+
+@pytest.mark.parametrize("page,D", [(16, 64), (64, 128), (32, 256)])
+def test_append_keeps_the_nan_of_pages_without_numbers(fq, page, D):
+    """NaN throughout a token, among zeros, and zeros alone, then numbers: the NaN codes stay what they are."""
+    rng = np.random.default_rng(page + D)
+    heads = 3
+    cache = random_cache(rng, 3, heads, page, D)
+    dev = up(cache)
+    table = np.array([[1]], np.int32)
+    for t in range(5):
+        k, v = bf16(rng, 1, heads, D), bf16(rng, 1, heads, D, gain=100.0)
+        if t < 3:  # head 0: NaN; head 1: NaN among zeros of both signs; head 2: numbers
+            for x in (k, v):
+                x[:, 0] = float("nan") if t != 1 else 0.0
+                x[:, 1] = -0.0
+                x[:, 1, t::5] = float("nan")
+        fq.kv_append_fp8(k, v, *dev, i32(table.tolist()), i32([0, 1]), i32([t + 1]), 1)
+        cache = fp8.kv_append(host(k), host(v), cache, table, [0, 1], [t + 1])
+        for got, w, name in zip(dev, cache, ("k", "v", "k_scale", "v_scale")):
+            assert np.array_equal(to_np(got), w), (t, name)
+        for codes in dev[:2]:
+            kept = to_np(codes)[1, :, :t + 1]
+            assert (kept[0, 0] == 0x7F).all() and (kept[1, 0, ::5] == 0x7F).all()
+            assert not np.delete(kept[1, 0], np.s_[::5]).any() and not (t and kept[0, 1].any())
+        assert t >= 3 or not (to_np(dev[2])[1, :2].any() or to_np(dev[3])[1, :2].any())
+    q = bf16(rng, 1, heads, D)
+    o, _ = fq.attention_fp8(q, *dev, i32(table.tolist()), i32([0, 1]), i32([5]), 1, 5)
+    o = to_np(o.float())[0]
+    assert np.isnan(o[:2]).all() and np.isfinite(o[2]).all()

@@ -89,3 +89,17 @@ def test_a_nan_keeps_its_code_where_the_scale_is_zero(tile):
     codes, scales = fp8.quantize(x, tile)
     assert not scales.any() and np.array_equal(codes, np.where(np.isnan(x), 0x7F, 0))
     assert np.array_equal(np.isnan(fp8.values(codes, scales, tile)), np.isnan(x))
+
+
+def test_append_keeps_the_nan_of_a_page_without_numbers():
+    """From a first token of NaN, zeros behind it, and a number that gives the page its scale."""
+    k = np.full((1, 1, 64), np.nan, np.float32)
+    k[..., :8] = -0.0
+    cache = [np.zeros((1, 1, 16, 64), np.uint8) for _ in range(2)] + [np.zeros((1, 1), np.float32) for _ in range(2)]
+    table = np.array([[0]])
+    first = np.where(np.arange(64) < 8, 0, 0x7F)
+    for t, x in enumerate((k, np.zeros_like(k), np.full_like(k, 448.0))):
+        fp8.kv_append(x, x, cache, table, np.array([0, 1]), np.array([t + 1]))
+        for codes, scale in ((cache[0], cache[2]), (cache[1], cache[3])):
+            assert np.array_equal(codes[0, 0, 0], first) and scale[0, 0] == (1 if t == 2 else 0)
+    assert not cache[0][0, 0, 1].any() and (cache[0][0, 0, 2] == 0x7E).all()
