@@ -75,13 +75,20 @@ __device__ __forceinline__ int32_t attn_page(const AttnParams& p, int64_t b, int
 // Softmax, one pass: with the page's V scale vs, the weights enter P V as
 // w = exp2(s + log2 vs - m) 2^14 <= 2^14, m the running maximum of s + log2 vs,
 // in fp16: full precision whatever the V scales are, and down to 2^-28 of the
-// largest before fp16's subnormals.  The denominator sums w / vs in fp32.
+// largest before fp16's subnormals.  The denominator sums w 2^-14 / vs in fp32.
+// Neither passes fp32's range for scales up to 2^127: the exponential is
+// e = exp2(s - m + 24), so that it keeps 2^-23 of a row's largest under them (its
+// subnormals are flushed), w = e (vs 2^-10), and e 2^-24 goes into the denominator.
+// Sums move to a new maximum by h = exp2((m - m') / 2) twice: a denominator is far
+// above 1 under a small V scale, and counts where h h itself is below fp32's range.
 //
 // 32 tokens over 6000 keys on average, 8 K/V heads of 128 in groups of 4: 76 us,
 // 0.80 of the copy rate (the codes' conversion keeps the ALU at 42 %); one token
 // over 500 7.5 us, the latency of its steps.
 
-constexpr float kAttnWeightLog2 = 14.0f;
+constexpr float kAttnLift = 24.0f, kAttnUnlift = 0x1p-24f;  // exponentials are 2^24 of what they stand for
+constexpr float kAttnWeight = 0x1p-10f;                     // and weights 2^14: 2^24 of them in the exponential
+constexpr float kAttnUnweight = 0x1p-14f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -421,11 +428,12 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
         if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {
             const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
-            const float a0 = n0 == -INFINITY ? 1.0f : exp2_approx(m0 - n0), a1 = n1 == -INFINITY ? 1.0f : exp2_approx(m1 - n1);
+            const float h0 = n0 == -INFINITY ? 1.0f : exp2_approx(0.5f * (m0 - n0)), h1 = n1 == -INFINITY ? 1.0f : exp2_approx(0.5f * (m1 - n1));
+            const float a0 = h0 * h0, a1 = h1 * h1;
             m0 = n0;
             m1 = n1;
-            l0 *= a0;
-            l1 *= a1;
+            l0 = l0 * h0 * h0;
+            l1 = l1 * h1 * h1;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 o[j][0] *= a0;
@@ -434,17 +442,17 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
                 o[j][3] *= a1;
             }
         }
-        const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+        const float b0 = (m0 == -INFINITY ? 0.0f : m0) - kAttnLift, b1 = (m1 == -INFINITY ? 0.0f : m1) - kAttnLift;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[j][i] = exp2_approx(x[j][i] - b0);
                 x[j][4 + i] = exp2_approx(x[j][4 + i] - b1);
-                l0 += x[j][i];
-                l1 += x[j][4 + i];
+                l0 = fmaf(x[j][i], kAttnUnlift, l0);
+                l1 = fmaf(x[j][4 + i], kAttnUnlift, l1);
             }
-            const float wv = vs[page[j]] * 0x1p14f;
+            const float wv = vs[page[j]] * kAttnWeight;
             const uint32_t p0 = f16x2_pack(x[j][0] * wv, x[j][1] * wv), p1 = f16x2_pack(x[j][4] * wv, x[j][5] * wv),
                            p2 = f16x2_pack(x[j][2] * wv, x[j][3] * wv), p3 = f16x2_pack(x[j][6] * wv, x[j][7] * wv);
             uint32_t vf[4][D / 32];  // codes of this lane: keys 2t, 2t+1, 8+2t, 9+2t
@@ -519,7 +527,10 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red_m[w][r]);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) l += red_m[w][r] == -INFINITY ? red_l[w][r] : red_l[w][r] * exp2_approx(red_m[w][r] - top);
+        for (int w = 0; w < kWarps; ++w) {
+            const float h = red_m[w][r] == -INFINITY ? 1.0f : exp2_approx(0.5f * (red_m[w][r] - top));
+            l = fmaf(red_l[w][r] * h, h, l);
+        }
         float v[D / 32];
 #pragma unroll
         for (int d = 0; d < D / 32; ++d) {
@@ -538,7 +549,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
         } else {
             const uint32_t row = r0 + r, i = row / (uint32_t)p.group;
             const int64_t tok = s.first + i, h = hk * p.group + (row - i * p.group);
-            const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
+            const float inv = l == 0.0f ? 0.0f : kAttnUnweight / l;
             uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + lane * (D / 32));
 #pragma unroll
             for (int d = 0; d < D / 32; d += 2) dst[d / 2] = bf16x2_pack(v[d] * inv, v[d + 1] * inv);
@@ -560,14 +571,14 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (i >= (int)sp.splits) break;
-                const float a = m[i] == -INFINITY ? 1.0f : exp2_approx(m[i] - top);
-                l = fmaf(z[i], a, l);
+                const float h = m[i] == -INFINITY ? 1.0f : exp2_approx(0.5f * (m[i] - top)), a = h * h;
+                l = fmaf(z[i] * h, h, l);
 #pragma unroll
                 for (int d = 0; d < D / 32; ++d) v[d] = fmaf(ld_cluster(slot + 4 * (lane * (D / 32) + d), i), a, v[d]);
             }
             const uint32_t row = r0 + r, i = row / (uint32_t)p.group;
             const int64_t tok = s.first + i, h = hk * p.group + (row - i * p.group);
-            const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
+            const float inv = l == 0.0f ? 0.0f : kAttnUnweight / l;
             uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + lane * (D / 32));
 #pragma unroll
             for (int d = 0; d < D / 32; d += 2) dst[d / 2] = bf16x2_pack(v[d] * inv, v[d + 1] * inv);
@@ -614,15 +625,15 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, cons
             for (int d = 0; d < D / 32; ++d) x[k][d] = i < n ? slot[lane * (D / 32) + d] : 0.0f;
         }
         const float t4 = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
-        const float keep = top == -INFINITY ? 1.0f : exp2_approx(top - t4);  // (nothing, or NaN, so far)
-        l *= keep;
+        const float hk = top == -INFINITY ? 1.0f : exp2_approx(0.5f * (top - t4)), keep = hk * hk;  // (nothing, or NaN, so far)
+        l = l * hk * hk;
 #pragma unroll
         for (int d = 0; d < D / 32; ++d) v[d] *= keep;
         top = t4;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float a = m[k] == -INFINITY ? 1.0f : exp2_approx(m[k] - top);
-            l = fmaf(z[k], a, l);
+            const float h = m[k] == -INFINITY ? 1.0f : exp2_approx(0.5f * (m[k] - top)), a = h * h;
+            l = fmaf(z[k] * h, h, l);
 #pragma unroll
             for (int d = 0; d < D / 32; ++d) v[d] = fmaf(x[k][d], a, v[d]);
         }
@@ -641,14 +652,14 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, cons
     l = 0.0f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        const float a = part[w][D] == -INFINITY ? 1.0f : exp2_approx(part[w][D] - top);
-        l = fmaf(part[w][D + 1], a, l);
+        const float h = part[w][D] == -INFINITY ? 1.0f : exp2_approx(0.5f * (part[w][D] - top)), a = h * h;
+        l = fmaf(part[w][D + 1] * h, h, l);
         x0 = fmaf(part[w][d], a, x0);
         x1 = fmaf(part[w][d + 1], a, x1);
     }
     const uint32_t i = (uint32_t)row / (uint32_t)p.group;
     const int64_t tok = s.first + i, h = hk * p.group + (row - i * p.group);
-    const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
+    const float inv = l == 0.0f ? 0.0f : kAttnUnweight / l;
     *reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + d) = bf16x2_pack(x0 * inv, x1 * inv);
     if (p.lse && threadIdx.x == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
 }

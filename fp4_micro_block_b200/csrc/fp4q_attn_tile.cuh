@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(640, 1)
                     tma_load_2d(dst + G::k8, &map_v, 0, row, full8 + 8 * st);
                 }
                 // (scales below 2^-100, and 0, weigh as 2^-100 in the maximum only)
-                if (lane < 8) run_scale[j & 7][lane] = make_float4(ks, vs * 0x1p14f, log2f(fmaxf(vs, 0x1p-100f)), 0.0f);
+                if (lane < 8) run_scale[j & 7][lane] = make_float4(ks, vs * kAttnWeight, log2f(fmaxf(vs, 0x1p-100f)), 0.0f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full8 + 8 * st);
             }
@@ -320,13 +320,13 @@ __global__ void __launch_bounds__(640, 1)
                     top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), sc[run].x * qs, sc[run].z));  // (-inf * 0 is no number: skipped)
                 }
             }
-            const float mn = fmaxf(m, top), a = mn == -INFINITY ? 1.0f : exp2_approx(m - mn), base = mn == -INFINITY ? 0.0f : mn;
+            const float mn = fmaxf(m, top), h = mn == -INFINITY ? 1.0f : exp2_approx(0.5f * (m - mn)), base = mn == -INFINITY ? 0.0f : mn;
             m = mn;
-            l *= a;
+            l = l * h * h;
             mref[(j & 3) * kTileRows + t] = mn;
             // P goes where S was: columns c .. of P overwrite columns of S that have been read
             uint64_t sum = 0;
-            const uint64_t nb = f2_both(-base);
+            const uint64_t nb = f2_both(kAttnLift - base);
             auto weights = [&](auto&& seen) {
 #pragma unroll 1
                 for (int col = 0; col < kTileKeys; col += 32) {
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(640, 1)
                             const uint64_t z = f2_fma(f2_pack(x[16 * h + i], x[16 * h + i + 1]), f, nb);
                             const uint64_t e = f2_pack(__float_as_uint(seen(16 * h + i, left - col, exp2_approx(f2_lo(z)))),
                                                        __float_as_uint(seen(16 * h + i + 1, left - col, exp2_approx(f2_hi(z)))));
-                            sum = f2_add(sum, e);
+                            sum = f2_fma(e, f2_both(kAttnUnlift), sum);
                             const uint64_t y = f2_mul(e, wv);
                             w[8 * h + i / 2] = f16x2_pack(f2_lo(y), f2_hi(y));
                         }
@@ -401,7 +401,8 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const float mk = ml[2 * k * kTileRows + t];
-            l = fmaf(ml[(2 * k + 1) * kTileRows + t], mk == -INFINITY ? 1.0f : exp2_approx(mk - mo), l);
+            const float h = mk == -INFINITY ? 1.0f : exp2_approx(0.5f * (mk - mo));
+            l = fmaf(ml[(2 * k + 1) * kTileRows + t] * h, h, l);
         }
         const int lim = attn_limit(p, s, r);
         if constexpr (SPLIT) {
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(640, 1)
                 if (t < rows) *reinterpret_cast<float2*>(slots + (int64_t)t * sp.splits * kAttnSlot<D> + D) = make_float2(mo, l);
             }
         } else if (t < rows) {
-            const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
+            const float inv = l == 0.0f ? 0.0f : kAttnUnweight / l;
             const uint32_t tok = (uint32_t)r / (uint32_t)p.group, h = hk * p.group + (r - tok * p.group);
             uint4* dst = reinterpret_cast<uint4*>(p.o + (s.first + tok) * p.ldo + (int64_t)h * D);
 #pragma unroll

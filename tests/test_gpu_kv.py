@@ -732,3 +732,66 @@ def test_append_keeps_the_nan_of_pages_without_numbers(fq, page, D):
     o, _ = fq.attention_fp8(q, *dev, i32(table.tolist()), i32([0, 1]), i32([5]), 1, 5)
     o = to_np(o.float())[0]
     assert np.isnan(o[:2]).all() and np.isfinite(o[2]).all()
+
+
+# (sequences, queries, keys, heads, group): 16 rows a CTA, alone, in a cluster and joined by a second kernel; 128 rows a
+# CTA, alone and with the keys split.  The last page of 32 holds the last key alone, which only the last query sees.
+LAST_ALONE = [(1, 1, 33, 1, 1), (2, 4, 97, 1, 2), (1, 4, 513, 1, 2), (1, 4, 9985, 1, 2), (24, 40, 193, 1, 2), (1, 128, 2017, 2, 4)]
+
+
+def moderate(cache):
+    """V codes of magnitudes up to 1, so that values stay in range under the largest scales."""
+    cache[1] = (cache[1] & 0x80) | np.minimum(cache[1] & 0x7F, 0x38)
+    return cache
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 114, 2.0 ** 120, 2.0 ** 127])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,new,L,heads,G", LAST_ALONE)
+def test_a_large_page_scale_of_v_reaches_only_those_who_see_it(fq, B, new, L, heads, G, D, scale):
+    """The other queries' results keep their bits; the last one's is the formula's."""
+    rng = np.random.default_rng(L + D)
+    page = 32
+    cache, table, cu, q = batch_of(fq, rng, B, new, L, page, D, heads, G)
+    moderate(cache)
+    args = (i32(table.tolist()), i32(cu), i32([L] * B), new, L)
+    clean = fq.attention_fp8(q, *up(cache), *args)
+    cache[3][table[:, (L - 1) // page]] = scale
+    o, lse = fq.attention_fp8(q, *up(cache), *args)
+    first = np.delete(np.arange(cu[-1]), np.array(cu[1:]) - 1)
+    assert torch.equal(o[first], clean[0][first]) and torch.equal(lse[first], clean[1][first])
+    compare(o, lse, q, cache, table, cu, [L] * B, True, D ** -0.5)
+
+
+@pytest.mark.parametrize("B,new,L,heads,G", LAST_ALONE)
+@pytest.mark.parametrize("D", [64, 128])
+def test_page_scales_of_v_up_to_the_largest(fq, B, new, L, heads, G, D):
+    """Every page large, and large pages among ordinary and tiny ones, all of them seen: o and lse are the formula's."""
+    rng = np.random.default_rng(L + D)
+    cache, table, cu, q = batch_of(fq, rng, B, new, L, 32, D, heads, G)
+    moderate(cache)
+    for exponents in ([114, 117, 120, 127], [120], [0, 120, -3, -100], [60, -60, 90, 0], [0, -90, -100]):
+        cache[3][:] = np.exp2(rng.choice(exponents, cache[3].shape)).astype(np.float32)
+        o, lse = fq.attention_fp8(q, *up(cache), i32(table.tolist()), i32(cu), i32([L] * B), new, L)
+        compare(o, lse, q, cache, table, cu, [L] * B, True, D ** -0.5)
+
+
+@pytest.mark.parametrize("B,new,L,heads,G", LAST_ALONE[1:])
+@pytest.mark.parametrize("side", [0, 1])
+def test_an_infinity_in_the_last_token_reaches_only_its_query(fq, B, new, L, heads, G, side):
+    """Through the append, which gives its page the scale 2^120."""
+    rng = np.random.default_rng(L + side)
+    page, D = 32, 128
+    cache, table, cu, q = batch_of(fq, rng, B, new, L, page, D, heads, G)
+    k, v = bf16(rng, cu[-1], heads, D), bf16(rng, cu[-1], heads, D)
+    args = (i32(table.tolist()), i32(cu), i32([L] * B))
+    outs = []
+    for broken in (False, True):
+        if broken:
+            (k, v)[side][np.array(cu[1:]) - 1, :, 5] = float("inf")
+        dev = up(cache)
+        fq.kv_append_fp8(k, v, *dev, *args, new)
+        assert not broken or (to_np(dev[2 + side])[table[:, (L - 1) // page]] == 2.0 ** 120).all()
+        outs.append(fq.attention_fp8(q, *dev, *args, new, L))
+    first = np.delete(np.arange(cu[-1]), np.array(cu[1:]) - 1)
+    assert torch.equal(outs[0][0][first], outs[1][0][first]) and torch.equal(outs[0][1][first], outs[1][1][first])
