@@ -55,6 +55,13 @@ __device__ __forceinline__ int32_t attn_page(const AttnParams& p, int64_t b, int
     return id;
 }
 
+// A page's scales of K and V as the kernels use them.  A V scale that is no number
+// (or infinite) would turn the weights of masked keys, which are 0, to NaN: the
+// page's scores are NaN in its place, which masking replaces.
+__device__ __forceinline__ float2 attn_page_scales(float ks, float vs) {
+    return fabsf(vs) < INFINITY ? make_float2(ks, vs) : make_float2(NAN, 0.0f);
+}
+
 // ------------------------------------------------------------------ few queries
 //
 // One CTA: one sequence, one K/V head, 16 rows (query i, head g of the group:
@@ -305,8 +312,9 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
     for (int i = threadIdx.x; i < n_pages; i += 32 * kWarps) {
         const int64_t at = attn_page(p, b, page0 + i, true) * p.c.heads + hk;
         ids[i] = (int32_t)at;
-        ks[i] = p.c.k_scale[at] * p.scale_log2;
-        vs[i] = p.c.v_scale[at];
+        const float2 f = attn_page_scales(p.c.k_scale[at], p.c.v_scale[at]);
+        ks[i] = f.x * p.scale_log2;
+        vs[i] = f.y;
         lvs[i] = log2f(fmaxf(vs[i], 0x1p-100f));  // scales below 2^-100 (and 0) weigh as 2^-100 in the maximum only
     }
 

@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(640, 1)
                     tma_load_2d(dst + G::k8, &map_v, 0, row, full8 + 8 * st);
                 }
                 // (scales below 2^-100, and 0, weigh as 2^-100 in the maximum only)
-                if (lane < 8) run_scale[j & 7][lane] = make_float4(ks, vs * kAttnWeight, log2f(fmaxf(vs, 0x1p-100f)), 0.0f);
+                const float2 f = attn_page_scales(ks, vs);
+                if (lane < 8) run_scale[j & 7][lane] = make_float4(f.x, f.y * kAttnWeight, log2f(fmaxf(f.y, 0x1p-100f)), 0.0f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full8 + 8 * st);
             }

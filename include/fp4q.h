@@ -369,7 +369,8 @@ fp4q_status fp4q_gemm_fp8(const uint8_t* a_codes, int64_t lda, const float* a_sc
 
 /* A paged K/V cache in 8 bits.  Page p of K holds page_size tokens of every
  * K/V head: codes uint8 [num_pages, num_kv_heads, page_size, head_dim], scales
- * float [num_pages, num_kv_heads] (value = E4M3(code) * scale); V likewise.
+ * float [num_pages, num_kv_heads], not negative (value = E4M3(code) * scale); V
+ * likewise.
  * Position t of sequence b lives in page block_table[b * table_stride +
  * t / page_size], row t % page_size.  page_size is 16, 32, 64 or 128; head_dim
  * 64, 128 or 256. */
@@ -424,8 +425,9 @@ fp4q_status fp4q_kv_append_fp8(const void* k, int64_t ldk, const void* v, int64_
  *            aligned; calls that may overlap need one each.
  * A query that sees no key gets o = 0 and lse = -inf.  Rows of o and lse outside
  * cu_q's ranges are left as they are.  Codes of masked keys, NaN codes among
- * them, do not reach a result.  Sums and softmax statistics are FP32; the
- * probabilities enter the product with V in FP16 under a common exponent.
+ * them, and scales of pages whose keys are all masked do not reach a result.
+ * Sums and softmax statistics are FP32; the probabilities enter the product with
+ * V in FP16 under a common exponent.
  * Entries out of range on the device are clamped (a page id outside
  * [0, num_pages) reads page 0) and reported through fp4q_device_error(), code 2. */
 fp4q_status fp4q_attention_fp8(const void* q, int64_t ldq, int64_t tokens, int32_t num_q_heads,

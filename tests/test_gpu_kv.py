@@ -795,3 +795,23 @@ def test_an_infinity_in_the_last_token_reaches_only_its_query(fq, B, new, L, hea
         outs.append(fq.attention_fp8(q, *dev, *args, new, L))
     first = np.delete(np.arange(cu[-1]), np.array(cu[1:]) - 1)
     assert torch.equal(outs[0][0][first], outs[1][0][first]) and torch.equal(outs[0][1][first], outs[1][1][first])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,new,L,heads,G", LAST_ALONE)
+def test_a_page_scale_that_is_no_number_reaches_only_those_who_see_it(fq, B, new, L, heads, G, D, bad):
+    rng = np.random.default_rng(L + D)
+    page = 32
+    cache, table, cu, q = batch_of(fq, rng, B, new, L, page, D, heads, G)
+    args = (i32(table.tolist()), i32(cu), i32([L] * B), new, L)
+    clean = fq.attention_fp8(q, *up(cache), *args)
+    last = np.array(cu[1:]) - 1
+    first = np.delete(np.arange(cu[-1]), last)
+    for side in (2, 3):
+        broken = [c.copy() for c in cache]
+        broken[side][table[:, (L - 1) // page]] = bad
+        o, lse = fq.attention_fp8(q, *up(broken), *args)
+        assert torch.equal(o[first], clean[0][first]) and torch.equal(lse[first], clean[1][first])
+        # (an infinite scale of K leaves scores of -inf, which are no NaN)
+        assert torch.isnan(o[last]).all() or (side == 2 and bad == float("inf"))
