@@ -370,11 +370,20 @@ bool attn_take_tile(int64_t row_items, int64_t tile_items, int64_t max_len, int6
     return by_tile < by_rows;
 }
 
+// Rows and keys are counted in 31 bits, with room for the last tile, and so are
+// the row tiles of a call (of 128 rows here; the kernel of 16 needs more room,
+// attn_plan).  Everything else that attn_plan multiplies stays within 64 bits then.
+fp4q_status attn_bounds(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_heads, int64_t kv_heads) {
+    if (max_len > kAttnMost || max_q > kAttnMost / (q_heads / kv_heads)) return FP4Q_ERR_UNSUPPORTED;
+    const int64_t heads = batch * kv_heads;  // (each below 2^31)
+    if (heads >= kMaxDim || heads * spans(max_q * (q_heads / kv_heads), kTileRows) >= kMaxDim) return FP4Q_ERR_UNSUPPORTED;
+    return FP4Q_OK;
+}
+
+// For sizes that attn_bounds takes.
 fp4q_status attn_plan(int64_t batch, int64_t max_q, int64_t max_len, int64_t q_heads, int64_t kv_heads, int64_t dim,
                       int sms, AttnPlan* out) {
     AttnPlan a{};
-    // rows and keys are counted in 31 bits, with room for the last tile
-    if (max_len > kAttnMost || max_q > kAttnMost / (q_heads / kv_heads)) return FP4Q_ERR_UNSUPPORTED;
     const int64_t rows = max_q * (q_heads / kv_heads), heads = batch * kv_heads;
     a.tile = dim <= 128 && attn_take_tile(heads * spans(rows, kAttnRows), heads * spans(rows, kTileRows), max_len, rows, sms);
     a.tile_rows = a.tile ? kTileRows : kAttnRows;
@@ -464,7 +473,7 @@ FP4Q_API size_t fp4q_attention_fp8_workspace_bytes(int64_t batch, int64_t max_q,
     if (batch == 0 || max_q == 0) return 0;
     int sms = 0;
     AttnPlan a;
-    if (sm_count(&sms) != FP4Q_OK ||
+    if (attn_bounds(batch, max_q, max_len, num_q_heads, num_kv_heads) != FP4Q_OK || sm_count(&sms) != FP4Q_OK ||
         attn_plan(batch, max_q, max_len, num_q_heads, num_kv_heads, head_dim, sms, &a) != FP4Q_OK)
         return bad;
     return a.ws_bytes;
@@ -509,6 +518,7 @@ FP4Q_API fp4q_status fp4q_attention_fp8(const void* q, int64_t ldq, int64_t toke
     p.lse = lse;
     int sms = 0;
     AttnPlan a;
+    if ((st = attn_bounds(batch, max_q, max_len, num_q_heads, p.c.heads)) != FP4Q_OK) return st;
     if ((st = sm_count(&sms)) != FP4Q_OK) return st;
     if ((st = attn_plan(batch, max_q, max_len, num_q_heads, p.c.heads, p.c.dim, sms, &a)) != FP4Q_OK) return st;
     if (a.ws_bytes > 0) {

@@ -146,3 +146,18 @@ def test_binding_refuses_codes_without_scales(fq):
     for out in ((codes, None), (None, scales), (codes, scales, codes, None), (codes, scales, None, scales)):
         with pytest.raises(ValueError, match="together"):
             fq.fp4q_quantize_fp8(x, fq.FP4Q_FP8_ROW, *out)
+
+
+def test_attention_refuses_work_that_31_bits_do_not_count(fq):
+    """Before anything of the device is asked: the products of batch, heads and row tiles themselves may pass 64 bits."""
+    c = cache(fq, num_kv_heads=65536)
+    row = 65536 * 128
+    call = lambda batch, max_q, max_len, heads: fq.lib().fp4q_attention_fp8(  # noqa: E731
+        X, row * heads // 65536, 5, heads, C.addressof(c), CU, LENS, batch, max_q, max_len, 1, 0.1, D,
+        row * heads // 65536, None, None, 0, None)
+    assert call(1 << 30, 1 << 25, 64, 65536) == fq.FP4Q_ERR_UNSUPPORTED
+    assert call(1 << 30, 1, 64, 65536) == fq.FP4Q_ERR_UNSUPPORTED
+    assert call(1, (1 << 30) + 1, 64, 65536) == fq.FP4Q_ERR_UNSUPPORTED
+    assert call(1, (1 << 29) + 1, 64, 131072) == fq.FP4Q_ERR_UNSUPPORTED
+    assert call(1, 1, (1 << 30) + 1, 65536) == fq.FP4Q_ERR_UNSUPPORTED
+    assert call(4, 1 << 23, 64, 65536) == fq.FP4Q_ERR_UNSUPPORTED

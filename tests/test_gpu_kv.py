@@ -815,3 +815,12 @@ def test_a_page_scale_that_is_no_number_reaches_only_those_who_see_it(fq, B, new
         assert torch.equal(o[first], clean[0][first]) and torch.equal(lse[first], clean[1][first])
         # (an infinite scale of K leaves scores of -inf, which are no NaN)
         assert torch.isnan(o[last]).all() or (side == 2 and bad == float("inf"))
+
+
+def test_the_largest_batches_and_head_counts(fq):
+    """Work that 31 bits do not count is refused, however the sizes make it up."""
+    big = 1 << 30
+    for sizes in ((big, 2048, 64, big, big, 128), (big, 1, 64, 4, 4, 128), (big, 1 << 25, 64, 65536, 65536, 64),
+                  (65536, 1, 64, 65536, 65536, 256), (4, big, 4096, 512, 512, 128)):
+        with pytest.raises(fq.Fp4qError):
+            fq.fp4q_attention_fp8_workspace_bytes(*sizes)
