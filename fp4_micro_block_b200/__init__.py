@@ -127,6 +127,15 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _ws_bytes(workspace) -> int:
+    """Bytes of a workspace (None: 0), which is written as one run from its pointer on."""
+    if workspace is None:
+        return 0
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -158,7 +167,7 @@ def fp4q_scales_bytes(M: int, ncols: int, layout: int = FP4Q_SCALES_LINEAR) -> i
 def fp4q_quantize_nvfp4(x, codes, scales, tensor_scale, mode=FP4Q_TSCALE_DYNAMIC,
                         layout=FP4Q_SCALES_LINEAR, workspace=None, stream=None):
     M, K = x.shape
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws_bytes = _ws_bytes(workspace)
     return _check(_lib.fp4q_quantize_nvfp4(_ptr(x), M, K, _ld(x), _ptr(codes), _ptr(scales),
                                            _ptr(tensor_scale), mode, layout, _ptr(workspace),
                                            ws_bytes, _stream(stream)), "fp4q_quantize_nvfp4")
@@ -182,7 +191,7 @@ def fp4q_hadamard_quantize(x, had_size, fmt, codes, scales, scale_fp32,
                            mode=FP4Q_TSCALE_DYNAMIC, layout=FP4Q_SCALES_LINEAR,
                            workspace=None, stream=None):
     M, K = x.shape
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws_bytes = _ws_bytes(workspace)
     return _check(_lib.fp4q_hadamard_quantize(_ptr(x), M, K, _ld(x), int(had_size), int(fmt),
                                               _ptr(codes), _ptr(scales), _ptr(scale_fp32), mode,
                                               layout, _ptr(workspace), ws_bytes, _stream(stream)),
@@ -194,7 +203,7 @@ def fp4q_arc_quantize(x, gamma, eps, perm, outliers, fmt, codes, scales, tensor_
                       stream=None):
     M, K = x.shape
     S = 0 if outliers is None else outliers.numel()
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws_bytes = _ws_bytes(workspace)
     return _check(_lib.fp4q_arc_quantize(_ptr(x), M, K, _ld(x), _ptr(gamma), float(eps), _ptr(perm),
                                          _ptr(outliers), S, int(fmt), _ptr(codes), _ptr(scales),
                                          _ptr(tensor_scale), mode, layout, _ptr(workspace),
@@ -231,7 +240,7 @@ def fp4q_hadamard_quantize_signed(x, had_size, signs, fmt, codes, scales, scale_
                                   mode=FP4Q_TSCALE_DYNAMIC, layout=FP4Q_SCALES_LINEAR,
                                   workspace=None, stream=None):
     M, K = x.shape
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws_bytes = _ws_bytes(workspace)
     keep, sp = _host_words(signs)
     return _check(_lib.fp4q_hadamard_quantize_signed(_ptr(x), M, K, _ld(x), int(had_size), sp, int(fmt),
                                                      _ptr(codes), _ptr(scales), _ptr(scale_fp32), mode,
@@ -425,6 +434,7 @@ def fp4q_attention_fp8_workspace_bytes(batch, max_q, max_len, num_q_heads, num_k
 def fp4q_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, max_q, max_len, o, lse=None,
                        causal=True, softmax_scale=None, workspace=None, stream=None):
     """o [tokens, Hq, D] (bf16) = attention of q [tokens, Hq, D] (bf16) over the cache."""
+    ws_bytes = _ws_bytes(workspace)
     dev = _device("fp4q_attention_fp8", q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, lens, o, lse, workspace)
     cache, _, dim, B = _kv_cache(k_cache, v_cache, k_scale, v_scale, block_table)
     T, Hq, _ = q.shape
@@ -434,10 +444,10 @@ def fp4q_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q,
         _want(lse, "lse", _F32, T, Hq)
         raise ValueError("lse must be contiguous")
     scale = dim ** -0.5 if softmax_scale is None else float(softmax_scale)
-    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return _launch("fp4q_attention_fp8", dev, _lib.fp4q_attention_fp8,
                    (q.data_ptr(), ldq, T, Hq, cache, cu_q.data_ptr(), lens.data_ptr(), B, int(max_q), int(max_len), bool(causal),
-                    scale, o.data_ptr(), ldo, None if lse is None else lse.data_ptr(), ws, ws_bytes), stream)
+                    scale, o.data_ptr(), ldo, None if lse is None else lse.data_ptr(),
+                    None if workspace is None else workspace.data_ptr(), ws_bytes), stream)
 
 
 # ----------------------------------------------------------------------------- allocating helpers

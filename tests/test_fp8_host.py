@@ -161,3 +161,25 @@ def test_attention_refuses_work_that_31_bits_do_not_count(fq):
     assert call(1, (1 << 29) + 1, 64, 131072) == fq.FP4Q_ERR_UNSUPPORTED
     assert call(1, 1, (1 << 30) + 1, 65536) == fq.FP4Q_ERR_UNSUPPORTED
     assert call(4, 1 << 23, 64, 65536) == fq.FP4Q_ERR_UNSUPPORTED
+
+
+def test_every_workspace_is_contiguous(fq):
+    """A view with gaps, or one that repeats its elements, has fewer bytes behind its pointer than it counts or bytes
+    between them that are not its own."""
+    x = torch.zeros((16, 64), dtype=torch.bfloat16)
+    buf = torch.zeros(64, dtype=torch.uint8)
+    f = torch.zeros(1)
+    perm = torch.zeros(64, dtype=torch.int32)
+    kv = fq.alloc_kv_cache(3, 2, 16, 64, device="cpu")
+    table = torch.zeros((1, 2), dtype=torch.int32)
+    cu, lens = torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    q = torch.zeros((1, 4, 64), dtype=torch.bfloat16)
+    for ws in (buf[::2], buf[:1].expand(32768), buf.view(8, 8).t(), buf.view(8, 8)[:, :4]):
+        for call in (lambda: fq.fp4q_attention_fp8(q, *kv, table, cu, lens, 1, 16, q, workspace=ws),
+                     lambda: fq.attention_fp8(q, *kv, table, cu, lens, 1, 16, ws=ws),
+                     lambda: fq.fp4q_quantize_nvfp4(x, buf, buf, f, workspace=ws),
+                     lambda: fq.fp4q_hadamard_quantize(x, 64, fq.FP4Q_NVFP4, buf, buf, f, workspace=ws),
+                     lambda: fq.fp4q_hadamard_quantize_signed(x, 64, [1, 2], fq.FP4Q_NVFP4, buf, buf, f, workspace=ws),
+                     lambda: fq.fp4q_arc_quantize(x, perm, 1e-6, perm, None, fq.FP4Q_NVFP4, buf, buf, f, workspace=ws)):
+            with pytest.raises(ValueError, match="contiguous"):
+                call()
