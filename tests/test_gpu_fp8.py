@@ -331,3 +331,24 @@ def test_gemm_of_a_row_that_is_all_nan(fq, M):
     D = fq.gemm_fp8(*fq.quantize_fp8(x), *w)
     rest = [i for i in range(M) if i != M // 2]
     assert torch.isnan(D[M // 2]).all() and torch.equal(D[rest], clean[rest])
+
+
+# ------------------------------------------------------------------ bytes around an output; gradients against differences
+
+@pytest.mark.parametrize("M,N", [(1, 130), (20, 130), (200, 130), (200, 128), (200, 132), (300, 129)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("ldd", [137, 139, 144])
+def test_gemm_writes_nothing_around_its_output(fq, M, N, out, ldd):
+    """The output begins eight rows into a buffer (16-byte aligned whatever the row's length) and ends before it does."""
+    K = 200
+    a, b = operands(fq, M, N, K, True, 11)
+    flat = torch.full(((M + 16) * ldd,), 123.0, dtype=out, device="cuda")
+    at = 8 * ldd
+    d = flat.as_strided((M, N), (ldd, 1), at)
+    assert d.data_ptr() % 16 == 0 and 0 < at and at + (M - 1) * ldd + N < flat.numel()
+    fq.fp4q_gemm_fp8(*a, *b, fq.FP4Q_FP8_TILE, d)
+    check(d, *reference(a, b, True), K, f"ldd {ldd}")
+    rest = to_np(flat.float()).copy()
+    for r in range(M):
+        rest[at + r * ldd:at + r * ldd + N] = 123.0
+    assert (rest == 123.0).all()
