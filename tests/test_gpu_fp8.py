@@ -352,3 +352,37 @@ def test_gemm_writes_nothing_around_its_output(fq, M, N, out, ldd):
     for r in range(M):
         rest[at + r * ldd:at + r * ldd + N] = 123.0
     assert (rest == 123.0).all()
+
+
+def test_gradients_against_differences_along_the_gradient(fq):
+    """L(x + e/2) - L(x - e/2) = <dL/dx, e> for L = <x W^T, dy>, which is linear in x and in W, with e the signs of the
+    true gradient: the sum of its magnitudes, which a wrong gradient misses.
+
+    Tolerance.  With dx' = G' W' (G' = G + dG, W' = W + dW: the quantized operands),
+      <dx' - dx, e> = sum dG_in (e W^T)_in + sum dW_nk (G^T e)_nk + sum e dG dW.
+    A rounding to E4M3 is off by at most r = 2^-4 |v| + 2^-10 s (s the block's scale, at most max |v| / 448).  As sums
+    of independent bounded terms (e depends on neither rounding) the first two leave 6 sqrt(sum (bound of a term)^2)
+    with probability below 2 exp(-18) (Hoeffding); the products of two roundings are such a sum too.  The fp32 sums of
+    the GEMM add their worst case, (N + 4 ceil(N/128)) 2^-23 sum |G'| |W'|."""
+    M, N, K = 203, 264, 392
+    x, dy, w = activations(M, K, 23), activations(M, N, 24), activations(N, K, 25)
+    xq = fq.quantize_fp8(x, fq.FP4Q_FP8_ROW, True)
+    wq = fq.quantize_fp8(w, fq.FP4Q_FP8_TILE, True)
+    gq = fq.quantize_fp8(dy, fq.FP4Q_FP8_ROW, True)
+    dx = fq.gemm_fp8(*gq[:2], *wq[2:], fq.FP4Q_FP8_TILE, torch.float32)
+    dw = fq.gemm_fp8(*gq[2:], *xq[2:], fq.FP4Q_FP8_ROW, torch.float32)
+    X, W, G = (host(t).astype(np.float64) for t in (x, w, dy))
+    off = lambda v: 2.0 ** -4 * np.abs(v) + 2.0 ** -10 * np.abs(v).max() / 448  # noqa: E731
+    rss = lambda *terms: np.sqrt(sum((t ** 2).sum() for t in terms))  # noqa: E731
+    for got, part, left, right, loss in ((dx, X, G, W, lambda t: ((t @ W.T) * G).sum()), (dw, W, G.T, X, lambda t: ((X @ t.T) * G).sum())):
+        e = np.sign(left @ right)  # of the true gradient
+        diff = loss(part + 0.5 * e) - loss(part - 0.5 * e)
+        got = to_np(got.double())
+        n = left.shape[1]
+        both = np.sqrt(((off(left) ** 2).sum(0) * (off(right) ** 2).sum(1)).sum())
+        tol = 6 * (rss(off(left) * (e @ right.T), off(right) * (left.T @ e)) + both) + \
+            (n + 4 * -(-n // 128)) * 2.0 ** -23 * 1.2 * (np.abs(left) @ np.abs(right)).sum()
+        assert abs((got * e).sum() - diff) <= tol
+        # what this test is there to reject: no gradient, the negated one, one of another size or a row off
+        for wrong in (np.zeros_like(got), -got, 10 * got, 0.5 * got, np.roll(got, 1, 0)):
+            assert abs((wrong * e).sum() - diff) > tol
