@@ -734,9 +734,11 @@ def test_append_keeps_the_nan_of_pages_without_numbers(fq, page, D):
     assert np.isnan(o[:2]).all() and np.isfinite(o[2]).all()
 
 
-# (sequences, queries, keys, heads, group): 16 rows a CTA, alone, in a cluster and joined by a second kernel; 128 rows a
-# CTA, alone and with the keys split.  The last page of 32 holds the last key alone, which only the last query sees.
-LAST_ALONE = [(1, 1, 33, 1, 1), (2, 4, 97, 1, 2), (1, 4, 513, 1, 2), (1, 4, 9985, 1, 2), (24, 40, 193, 1, 2), (1, 128, 2017, 2, 4)]
+# (sequences, queries, keys, heads, group): 16 rows a CTA, alone, in a cluster and joined by a second kernel (one row tile
+# and many); 128 rows a CTA (head dims 64 and 128), alone and with the keys split.  The last page of 32 holds the last key
+# alone, which only the last query sees.
+LAST_ALONE = [(1, 1, 33, 1, 1), (2, 4, 97, 1, 2), (1, 4, 513, 1, 2), (1, 4, 9985, 1, 2), (1, 128, 2017, 2, 4), (24, 40, 193, 1, 2),
+              (2, 64, 1537, 8, 2)]
 
 
 def moderate(cache):
@@ -824,3 +826,21 @@ def test_the_largest_batches_and_head_counts(fq):
                   (65536, 1, 64, 65536, 65536, 256), (4, big, 4096, 512, 512, 128)):
         with pytest.raises(fq.Fp4qError):
             fq.fp4q_attention_fp8_workspace_bytes(*sizes)
+
+
+@pytest.mark.parametrize("B,new,L,heads,G", LAST_ALONE)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_nan_code_of_the_last_token_reaches_only_its_query(fq, B, new, L, heads, G, D):
+    rng = np.random.default_rng(L + D)
+    page = 32
+    cache, table, cu, q = batch_of(fq, rng, B, new, L, page, D, heads, G)
+    args = (i32(table.tolist()), i32(cu), i32([L] * B), new, L)
+    clean = fq.attention_fp8(q, *up(cache), *args)[0]
+    last = np.array(cu[1:]) - 1
+    for side in (0, 1):
+        broken = [c.copy() for c in cache]
+        broken[side][table[:, (L - 1) // page], :, 0, 3] = 0x7F
+        o = fq.attention_fp8(q, *up(broken), *args)[0]
+        bad = torch.zeros_like(o, dtype=torch.bool)
+        bad[last, :, slice(3, 4) if side else slice(None)] = True
+        assert torch.isnan(o[bad]).all() and torch.equal(o[~bad], clean[~bad]), side
