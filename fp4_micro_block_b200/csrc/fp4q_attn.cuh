@@ -19,6 +19,9 @@ struct AttnParams {
     uint16_t* o;
     int64_t ldo;
     float* lse;
+#ifdef FP4Q_TEST_HOOKS
+    int64_t skip_copy;       // withheld()
+#endif
 };
 
 constexpr float kLn2 = 0.693147180559945309f;
@@ -292,6 +295,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
         const uint32_t bar = full0 + 8 * stage;
         const int n = min(2, tiles - 2 * turn);
         mbar_arrive_expect_tx(bar, n * G::tile_bytes);
+        if (withheld(p, turn)) return;
         for (int j = 0; j < n; ++j) {
             const int tile = 2 * turn + j;
             const int32_t row = id(tile >> shift) * p.c.page + (tile & (per_page - 1)) * kAttnStep;

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(640, 1)
                 }
                 if (lane == 0) mbar_arrive_expect_tx(full8 + 8 * st, boxes * 2 * kAttnStep * D);
                 __syncwarp();
-                if (lane < boxes) {
+                if (lane < boxes && !withheld(p, j)) {
                     const int32_t row = (id * p.c.heads + hk) * p.c.page + ((8 * j + lane) & (per_page - 1)) * kAttnStep;
                     const uint32_t dst = smem_u32(smem + G::raw_off) + st * 2 * G::k8 + lane * kAttnStep * D;
                     tma_load_2d(dst, &map_k, 0, row, full8 + 8 * st);

@@ -34,6 +34,18 @@ using namespace fp4q;
 
 int64_t spans(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
+#ifdef FP4Q_TEST_HOOKS
+// Test build only: the copies that CTA 0 of the next launch of a kernel with TMA
+// loads withholds (-1: none); consumed by that launch.
+std::atomic<int64_t> g_test_skip_copy{-1};
+#endif
+template <typename P>
+void take_skip(P& p) {
+#ifdef FP4Q_TEST_HOOKS
+    p.skip_copy = g_test_skip_copy.exchange(-1);
+#endif
+}
+
 bool valid_block(fp4q_fp8_block b) { return b == FP4Q_FP8_ROW || b == FP4Q_FP8_TILE; }
 
 // One side of a quantized matrix: codes [rows, ld] and scales [ceil(cols/128), lds].
@@ -259,6 +271,7 @@ FP4Q_API fp4q_status fp4q_quantize_fp8(const void* x, int64_t M, int64_t K, int6
         const int grid = (int)std::min<int64_t>(spans(p.n_items, per), (int64_t)sms * 4);
         return launch(fp8_row_kernel, grid, kFp8RowThreads, 0, (cudaStream_t)stream, p);
     }
+    take_skip(p);
     p.n_items = spans(M, kFp8Block) * p.n_kb;
     if (p.n_items >= kMaxDim) return FP4Q_ERR_UNSUPPORTED;
     return block == FP4Q_FP8_TILE ? launch_fp8_tile<true>(p, (cudaStream_t)stream) : launch_fp8_tile<false>(p, (cudaStream_t)stream);
@@ -286,6 +299,7 @@ FP4Q_API fp4q_status fp4q_gemm_fp8(const uint8_t* a_codes, int64_t lda, const fl
     p.ldd = ldd;
     p.out_bf16 = d_bf16;
     p.split = 1;
+    take_skip(p);
     if (f8_take_wide(M, N, p.n_kb, b.tile != 0, sms)) {
         if (b.tile) return launch_f8_wide<false>(a, b, K, p, sms, (cudaStream_t)stream);
         return launch_f8_wide<true>(a, b, K, p, sms, (cudaStream_t)stream);
@@ -525,6 +539,7 @@ FP4Q_API fp4q_status fp4q_attention_fp8(const void* q, int64_t ldq, int64_t toke
         if (!workspace || workspace_bytes < a.ws_bytes) return FP4Q_ERR_INVALID_ARG;
         if (!aligned(workspace, 16)) return FP4Q_ERR_ALIGNMENT;
     }
+    take_skip(p);
     if (a.tile)
         return a.splits > 1 ? (p.c.dim == 64 ? launch_attn_tile<64, true> : launch_attn_tile<128, true>)(p, a, workspace, (cudaStream_t)stream)
                             : (p.c.dim == 64 ? launch_attn_tile<64, false> : launch_attn_tile<128, false>)(p, a, workspace, (cudaStream_t)stream);
@@ -532,3 +547,11 @@ FP4Q_API fp4q_status fp4q_attention_fp8(const void* q, int64_t ldq, int64_t toke
     if (p.c.dim == 128) return launch_attn<128>(p, a, workspace, (cudaStream_t)stream);
     return launch_attn<256>(p, a, workspace, (cudaStream_t)stream);
 }
+
+#ifdef FP4Q_TEST_HOOKS
+// Test build only (not declared in include/fp4q.h): makes CTA 0 of the next launch
+// of the two-way quantizer, the FP8 GEMM or the cache attention arm its barrier for
+// copies number i (a tile, a K block, a turn of 32 keys or a tile of 128) and never
+// issue them, so that the bounded waits for them run out.
+FP4Q_API void fp4q_test_skip_copy(int64_t i) { g_test_skip_copy.store(i); }
+#endif

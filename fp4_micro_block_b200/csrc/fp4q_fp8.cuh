@@ -151,6 +151,9 @@ struct Fp8QuantParams {
     float* scales_t;
     int64_t ldst;
     int64_t n_kb, n_items;  // 128-column blocks of a row; work items
+#ifdef FP4Q_TEST_HOOKS
+    int64_t skip_copy;       // withheld()
+#endif
 };
 
 // Eight bf16 of row r, columns c .. c + 7, as four words; zeros outside [0, M) x [0, K).
@@ -300,6 +303,7 @@ __global__ void __launch_bounds__(kFp8TileThreads, kFp8TileCtas)
         const uint32_t mb = item / n_kb, kb = item - mb * n_kb;
         const uint32_t dst = smem_u32(smem + stage * kFp8TileBytes), bar = full0 + 8 * stage;
         mbar_arrive_expect_tx(bar, kFp8TileBytes);
+        if (withheld(p, item / gridDim.x)) return;
         tma_load_2d(dst, &map_x, (int32_t)(kb * kFp8Block), (int32_t)(mb * kFp8Block), bar);
         tma_load_2d(dst + kFp8TileBytes / 2, &map_x, (int32_t)(kb * kFp8Block + 64), (int32_t)(mb * kFp8Block), bar);
     };

@@ -46,6 +46,9 @@ struct Fp8GemmParams {
     int32_t out_bf16;
     int32_t tma_store;       // wide kernel: D's rows begin and end on 16 bytes
     int32_t split;           // narrow kernel: CTAs of the cluster that share a tile's K blocks
+#ifdef FP4Q_TEST_HOOKS
+    int64_t skip_copy;       // withheld()
+#endif
 };
 
 // kind::f8f6f4 instruction descriptor: D fp32 (1 at [4,6)), A and B E4M3 (0 at
@@ -240,8 +243,10 @@ __global__ void __launch_bounds__(F8Narrow<NT>::threads, 1)
                 uint8_t* st = smem + s * G::stage_bytes;
                 const uint32_t bar = full0 + 8 * s;
                 mbar_arrive_expect_tx(bar, G::stage_bytes);
-                tma_load_2d(smem_u32(st), &map_l, (kb0 + g) * kFp8Block, (int32_t)(lt * kF8Lanes), bar);
-                tma_load_2d(smem_u32(st + kF8LaneBytes), &map_c, (kb0 + g) * kFp8Block, (int32_t)(ct * NT), bar);
+                if (!withheld(p, g)) {
+                    tma_load_2d(smem_u32(st), &map_l, (kb0 + g) * kFp8Block, (int32_t)(lt * kF8Lanes), bar);
+                    tma_load_2d(smem_u32(st + kF8LaneBytes), &map_c, (kb0 + g) * kFp8Block, (int32_t)(ct * NT), bar);
+                }
                 if (++s == S) {
                     s = 0;
                     ph ^= 1;
@@ -490,8 +495,10 @@ __global__ void __launch_bounds__(F8Wide::threads, 1)
                 uint8_t* st = smem + s * G::stage_bytes;
                 const uint32_t bar = full0 + 8 * s;
                 mbar_arrive_expect_tx(bar, G::stage_bytes);
-                tma_load_2d(smem_u32(st), &map_l, kb * kFp8Block, (int32_t)(lt * kF8Lanes), bar);
-                tma_load_2d(smem_u32(st + kF8LaneBytes), &map_c, kb * kFp8Block, (int32_t)(ct * NT), bar);
+                if (!withheld(p, g)) {
+                    tma_load_2d(smem_u32(st), &map_l, kb * kFp8Block, (int32_t)(lt * kF8Lanes), bar);
+                    tma_load_2d(smem_u32(st + kF8LaneBytes), &map_c, kb * kFp8Block, (int32_t)(ct * NT), bar);
+                }
                 if (++s == S) {
                     s = 0;
                     ph ^= 1;
