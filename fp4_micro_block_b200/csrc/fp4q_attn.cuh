@@ -60,9 +60,10 @@ __device__ __forceinline__ int32_t attn_page(const AttnParams& p, int64_t b, int
 
 // A page's scales of K and V as the kernels use them.  A V scale that is no number
 // (or infinite) would turn the weights of masked keys, which are 0, to NaN: the
-// page's scores are NaN in its place, which masking replaces.
+// page's scores are NaN in its place (vs - vs is 0 for numbers), which masking
+// replaces.  (As a select between the two it took a microsecond of 76.)
 __device__ __forceinline__ float2 attn_page_scales(float ks, float vs) {
-    return fabsf(vs) < INFINITY ? make_float2(ks, vs) : make_float2(NAN, 0.0f);
+    return make_float2(ks + (vs - vs), fminf(vs, 3.4028234e38f));
 }
 
 // ------------------------------------------------------------------ few queries
@@ -87,7 +88,7 @@ __device__ __forceinline__ float2 attn_page_scales(float ks, float vs) {
 // in fp16: full precision whatever the V scales are, and down to 2^-28 of the
 // largest before fp16's subnormals.  The denominator sums w 2^-14 / vs in fp32.
 // Neither passes fp32's range for scales up to 2^127: the exponential is
-// e = exp2(s - m + 24), so that it keeps 2^-23 of a row's largest under them (its
+// e = exp2(s - (m - 24)), so that it keeps 2^-23 of a row's largest under them (its
 // subnormals are flushed), w = e (vs 2^-10), and e 2^-24 goes into the denominator.
 // Sums move to a new maximum by h = exp2((m - m') / 2) twice: a denominator is far
 // above 1 under a small V scale, and counts where h h itself is below fp32's range.
@@ -99,6 +100,10 @@ __device__ __forceinline__ float2 attn_page_scales(float ks, float vs) {
 constexpr float kAttnLift = 24.0f, kAttnUnlift = 0x1p-24f;  // exponentials are 2^24 of what they stand for
 constexpr float kAttnWeight = 0x1p-10f;                     // and weights 2^14: 2^24 of them in the exponential
 constexpr float kAttnUnweight = 0x1p-14f;
+
+// log2 of a page's V scale as it enters the maxima, which are 24 below what they stand
+// for.  Scales below 2^-100 (and 0) weigh as 2^-100 in the maximum only.
+__device__ __forceinline__ float attn_log2_scale(float vs) { return log2f(fmaxf(vs, 0x1p-100f)) - kAttnLift; }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -196,9 +201,6 @@ struct AttnGeo {
     static constexpr int bar_off = ml_off + 2 * 4 * warps * kAttnRows;
     static constexpr int smem = 1024 + bar_off + 8 * warps * stages;
 };
-
-// Bytes of w that are NaN codes, as 0xff; the others 0.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
 // A NaN code of V reaches the rows that see its key and no other: it is taken out
 // of the product (vf), and the rows that see one are counted with products of 0s
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
         const float2 f = attn_page_scales(p.c.k_scale[at], p.c.v_scale[at]);
         ks[i] = f.x * p.scale_log2;
         vs[i] = f.y;
-        lvs[i] = log2f(fmaxf(vs[i], 0x1p-100f));  // scales below 2^-100 (and 0) weigh as 2^-100 in the maximum only
+        lvs[i] = attn_log2_scale(vs[i]);
     }
 
     // this lane's part of the queries: rows g and g + 8, dims D/4 t .. D/4 t + D/4 - 1, scaled by a power of two
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
                 o[j][3] *= a1;
             }
         }
-        const float b0 = (m0 == -INFINITY ? 0.0f : m0) - kAttnLift, b1 = (m1 == -INFINITY ? 0.0f : m1) - kAttnLift;
+        const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
             uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + lane * (D / 32));
 #pragma unroll
             for (int d = 0; d < D / 32; d += 2) dst[d / 2] = bf16x2_pack(v[d] * inv, v[d + 1] * inv);
-            if (p.lse && lane == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+            if (p.lse && lane == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + kAttnLift + log2f(l)) * kLn2;
         }
     }
     if (joined) {
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(32 * AttnGeo<D>::warps, AttnGeo<D>::ctas)
             uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + lane * (D / 32));
 #pragma unroll
             for (int d = 0; d < D / 32; d += 2) dst[d / 2] = bf16x2_pack(v[d] * inv, v[d + 1] * inv);
-            if (p.lse && lane == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+            if (p.lse && lane == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + kAttnLift + log2f(l)) * kLn2;
         }
         cluster_sync();  // no CTA leaves while another reads its slots
     }
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, cons
     const int64_t tok = s.first + i, h = hk * p.group + (row - i * p.group);
     const float inv = l == 0.0f ? 0.0f : kAttnUnweight / l;
     *reinterpret_cast<uint32_t*>(p.o + tok * p.ldo + h * D + d) = bf16x2_pack(x0 * inv, x1 * inv);
-    if (p.lse && threadIdx.x == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+    if (p.lse && threadIdx.x == 0) p.lse[tok * p.q_heads + h] = l == 0.0f ? -INFINITY : (top + kAttnLift + log2f(l)) * kLn2;
 }
 
 }  // namespace fp4q

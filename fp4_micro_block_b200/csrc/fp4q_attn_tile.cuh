@@ -189,9 +189,8 @@ __global__ void __launch_bounds__(640, 1)
                     tma_load_2d(dst, &map_k, 0, row, full8 + 8 * st);
                     tma_load_2d(dst + G::k8, &map_v, 0, row, full8 + 8 * st);
                 }
-                // (scales below 2^-100, and 0, weigh as 2^-100 in the maximum only)
                 const float2 f = attn_page_scales(ks, vs);
-                if (lane < 8) run_scale[j & 7][lane] = make_float4(f.x, f.y * kAttnWeight, log2f(fmaxf(f.y, 0x1p-100f)), 0.0f);
+                if (lane < 8) run_scale[j & 7][lane] = make_float4(f.x, f.y * kAttnWeight, attn_log2_scale(f.y), 0.0f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full8 + 8 * st);
             }
@@ -327,7 +326,7 @@ __global__ void __launch_bounds__(640, 1)
             mref[(j & 3) * kTileRows + t] = mn;
             // P goes where S was: columns c .. of P overwrite columns of S that have been read
             uint64_t sum = 0;
-            const uint64_t nb = f2_both(kAttnLift - base);
+            const uint64_t nb = f2_both(-base);
             auto weights = [&](auto&& seen) {
 #pragma unroll 1
                 for (int col = 0; col < kTileKeys; col += 32) {
@@ -449,7 +448,7 @@ __global__ void __launch_bounds__(640, 1)
                     if (nan_key[8 * c + i] < lim) v[i] = __int_as_float(0x7fffffff);
                 dst[c] = make_uint4(bf16x2_pack(v[0], v[1]), bf16x2_pack(v[2], v[3]), bf16x2_pack(v[4], v[5]), bf16x2_pack(v[6], v[7]));
             }
-            if (p.lse) p.lse[(s.first + tok) * p.q_heads + h] = l == 0.0f ? -INFINITY : (mo + log2f(l)) * kLn2;
+            if (p.lse) p.lse[(s.first + tok) * p.q_heads + h] = l == 0.0f ? -INFINITY : (mo + kAttnLift + log2f(l)) * kLn2;
         }
     } else {
         // ------------------------------------------------ conversion of the codes to fp16

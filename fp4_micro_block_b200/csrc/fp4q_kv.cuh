@@ -36,6 +36,9 @@ __device__ __forceinline__ float kv_inverse(float s) {
     return s == 0.0f ? 0.0f : __uint_as_float((254u << 23) - __float_as_uint(s));
 }
 
+// Bytes of w that are NaN codes, as 0xff; the others 0.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
 struct KvAppendParams {
     KvCacheView c;
     const uint16_t *k, *v;
@@ -109,15 +112,14 @@ __global__ void __launch_bounds__(kKvMaxThreads) kv_append_kernel(const KvAppend
     if (threadIdx.x == 0) *scale = s;
     if (s > old && from > 0) {  // what the page has moves to the new scale (under a scale of 0: zeros and NaN, which stay)
         const float ratio = old * inv;
-        const uint32_t sign = old > 0.0f ? ~0u : 0x7fffffffu;  // (a zero of such a page has code 0)
         for (int e = threadIdx.x; e < from << p.per_row_log2; e += blockDim.x) {
             uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)e * 8);
             const uint2 x = *at;
             float f[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                f[k] = __uint_as_float(__float_as_uint(e4m3_decode(((k < 4 ? x.x : x.y) >> (8 * (k & 3)))) * ratio) & sign);
-            *at = make_uint2(e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7]));
+            for (int k = 0; k < 8; ++k) f[k] = e4m3_decode(((k < 4 ? x.x : x.y) >> (8 * (k & 3)))) * ratio;
+            *at = old > 0.0f ? make_uint2(e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7]))
+                             : make_uint2(nan_bytes(x.x) & 0x7f7f7f7fu, nan_bytes(x.y) & 0x7f7f7f7fu);
         }
     }
     uint8_t* dst = codes + ((int64_t)from << (p.per_row_log2 + 3));
