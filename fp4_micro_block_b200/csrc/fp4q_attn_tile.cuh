@@ -19,7 +19,7 @@
 //                   under the larger of the two maxima;
 //             4     conversion.
 // Two chunks of 1000 queries over 4096 keys, 8 K/V heads of 128 in groups of 4:
-// 175 us, 573 TFLOP/s.  No pipe is full (tensor a third, ALU and exponentials
+// 173 to 175 us, 574 TFLOP/s.  No pipe is full (tensor a third, ALU and exponentials
 // nearly two fifths): the chain S, softmax, P V over two buffers bounds it.  Half
 // tiles of 64 keys with O in tensor memory took 195 us, K's conversion shared with
 // the output's warpgroup 177.
@@ -198,8 +198,7 @@ __global__ void __launch_bounds__(640, 1)
             for (int i = j > 2 ? j - 2 : 0; i < j; ++i) (void)mbar_wait(full8 + 8 * (i & 1), (uint32_t)((i >> 1) & 1));
         } else if (warp == 1 && tiles > 0) {
             // -------------------------------------------- MMA: S runs two tiles ahead of P V
-            // The whole warp goes through the loop, so that addresses stay in uniform
-            // registers, and one lane issues.
+            // The whole warp goes through the loop, and one lane issues.
             const bool one = elect_one();
             const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t kd = sw128_desc_lo(smem_u32(smem + G::kf_off)), vd = sw128_desc_lo(smem_u32(smem + G::vf_off));

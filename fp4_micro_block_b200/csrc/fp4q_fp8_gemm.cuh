@@ -18,8 +18,7 @@
 //
 // CTA roles: warp 0 lane 0 streams the K blocks of both operands by TMA into a
 // ring; warp 1 allocates TMEM and issues the MMAs (as a whole, one lane elected:
-// a branch on lane 0 kept the descriptors out of uniform registers, 158 us
-// against 141 for 8192x4096x4096); the other warps (groups of four, each with
+// 141 us for 8192x4096x4096, with a branch on lane 0 158); the other warps (groups of four, each with
 // its columns) scale and accumulate, then store.
 // Every wait is bounded; a wait that runs out sets g_device_error and the role
 // stops; the CTA drains its copies and MMAs and frees TMEM before it exits.
@@ -258,8 +257,7 @@ __global__ void __launch_bounds__(F8Narrow<NT>::threads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        // The whole warp goes through the loop, so that addresses stay in uniform
-        // registers, and one lane issues.
+        // The whole warp goes through the loop, and one lane issues.
         const bool one = elect_one();
         const uint32_t t0 = __shfl_sync(0xffffffffu, tmem_base, 0);
         const uint32_t ring = sw128_desc_lo(smem_u32(smem));
@@ -389,8 +387,9 @@ __global__ void __launch_bounds__(F8Narrow<NT>::threads, 1)
 
 // ------------------------------------------------------------------ wide kernel
 //
-// 8192x4096x4096 141 us (1.95 PFLOP/s) with tile scales, 195 us with row scales
-// and fp32 output (two multiplies a sum, column scales from shared memory).  The
+// 8192x4096x4096 139 to 142 us (1.97 to 1.94 PFLOP/s) with tile scales, 166 in a long
+// run under the power limit; 4096x4096x8190 with row scales and fp32 output (two
+// multiplies a sum, column scales from shared memory) 209 to 223, 234 so.  The
 // two TMEM buffers are all of tensor memory, and their hand-over between the MMAs
 // and the warps that scale bounds it: the tensor pipe is busy 45 % of the time.
 // Sixteen such warps took 159 us, CTA pairs 181.
@@ -514,8 +513,7 @@ __global__ void __launch_bounds__(F8Wide::threads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        // The whole warp goes through the loop, so that addresses stay in uniform
-        // registers, and one lane issues.
+        // The whole warp goes through the loop, and one lane issues.
         const bool one = elect_one();
         const uint32_t t0 = __shfl_sync(0xffffffffu, tmem_base, 0);
         const uint32_t ring = sw128_desc_lo(smem_u32(smem));

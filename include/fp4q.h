@@ -437,7 +437,9 @@ fp4q_status fp4q_attention_fp8(const void* q, int64_t ldq, int64_t tokens, int32
                                size_t workspace_bytes, fp4q_stream_t stream);
 
 /* Device scratch fp4q_attention_fp8 needs for these sizes (0: none; the
- * workspace may then be NULL).  Depends on the current device's SM count.
+ * workspace may then be NULL).  Depends on the current device's SM count.  Keys
+ * are split by the bounds, so a call with smaller bounds may need more: a
+ * workspace serves the bounds that it was asked for.
  * Returns (size_t)-1 on bad arguments. */
 size_t fp4q_attention_fp8_workspace_bytes(int64_t batch, int64_t max_q, int64_t max_len,
                                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
