@@ -267,17 +267,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     return false;
 }
 
-// Test build only: whether CTA 0 withholds the copies that it has armed its barrier
-// for the i-th time for (p.skip_copy, -1: none), so that the waits for them run out.
-template <typename P>
-__device__ __forceinline__ bool withheld(const P& p, int64_t i) {
-#ifdef FP4Q_TEST_HOOKS
-    return blockIdx.x == 0 && i == p.skip_copy;
-#else
-    return false;
-#endif
-}
-
 // 2-D tiled TMA load of one box into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t x,
                                             int32_t y, uint32_t bar) {

@@ -38,6 +38,17 @@ __device__ __forceinline__ Half4 e4m3x4_f16(uint32_t four) {
     return h;
 }
 
+// Test build only: whether CTA 0 withholds the copies that it has armed its barrier
+// for the i-th time for (p.skip_copy, -1: none), so that the waits for them run out.
+template <typename P>
+__device__ __forceinline__ bool withheld(const P& p, int64_t i) {
+#ifdef FP4Q_TEST_HOOKS
+    return blockIdx.x == 0 && i == p.skip_copy;
+#else
+    return false;
+#endif
+}
+
 // All CTAs of the cluster have arrived, and see each other's shared memory.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
